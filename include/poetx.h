@@ -306,6 +306,48 @@ poetx_status poetx_adamw_step(const poetx_adamw_cfg* cfg, long long n, int t, fl
  * restarts the moments with the parameters (their step count t starts again at 1). */
 poetx_status poetx_adamw_reset(long long n, float* m, float* v, poetx_stream stream);
 
+/* AdamW over many tensors at once (e.g. the packed theta of every layer of a model, with its norms and
+ * embeddings) in one launch per 448 tensors, with moments in fp32 or in 8 bits.  Per tensor
+ *   eta = gamma * lr * lr_scale,  decay = weight_decay * decay_scale,
+ * and per element, in float32 with one rounding per operation for the moments:
+ *   m <- beta1 m + (1 - beta1) g;   v <- beta2 v + ((1 - beta2) g) g;   r = sqrt(v);
+ *   p <- p - eta * (decay * p + (m / (1 - beta1^t)) / (r / sqrt(1 - beta2^t) + eps)).
+ * POETX_MOMENT_F32: m and v float32 [n]; scale unused.
+ * POETX_MOMENT_E4M3: POETX_MOMENT_BLOCK = 256 consecutive elements of the tensor (the last block may be
+ *   shorter) share scale[block] = {u_m, u_r} with u_m = max |m| / 448 and u_r = max r / 448; m and v hold one
+ *   e4m3 code per element (uint8 [n]; float8_e4m3fn of other libraries) with m = u_m * code(m) and
+ *   sqrt(v) = u_r * code(v).  All-zero codes and scales are the moments' start.  The step uses the moments
+ *   before they are rounded; r > 0 is never stored as 0 (at least 2^-9 u_r), so an element whose
+ *   gradients were seen is never divided by eps alone.  A block whose largest |m| is under 2^-100 stores
+ *   zeros; a NaN or infinite moment is stored as NaN and left out of its block's maximum.
+ * seed == 0 rounds codes and bf16 parameters to nearest, ties to even.  seed != 0 rounds them up with the
+ * probability of the part cut off, from 16 bits of a hash of (seed, position in `tensors`, element): with a
+ * new seed each step, changes below half a step of the grid (as (1 - beta2) makes them) add up instead of
+ * being lost.  The same arguments give the same bits. */
+#define POETX_MOMENT_BLOCK 256
+typedef enum { POETX_MOMENT_F32 = 0, POETX_MOMENT_E4M3 = 1 } poetx_moment;
+typedef struct {
+  void* param;              /* param_dtype [n] (in/out)                                        */
+  const void* grad;         /* grad_dtype [n] (in)                                             */
+  void* m;                  /* moments (in/out): float32 [n], or e4m3 codes uint8 [n]           */
+  void* v;
+  float* scale;             /* E4M3: float32 [ceil(n / 256), 2] (in/out), 8-byte aligned; else NULL */
+  long long n;              /* elements; 0: the tensor is skipped                              */
+  float lr_scale;           /* multiplies gamma * lr for this tensor (>= 0)                    */
+  float decay_scale;        /* multiplies weight_decay for this tensor (>= 0)                  */
+  poetx_dtype param_dtype;  /* POETX_F32 or POETX_BF16                                         */
+  poetx_dtype grad_dtype;   /* POETX_F32 or POETX_BF16                                         */
+  poetx_moment moment;
+} poetx_adamw_tensor;
+
+/* One step of all tensors; t >= 1 is the step count of the moments.  `tensors` is a HOST array read
+ * during the call (it may be freed after it, also under stream capture).  Array pointers are 16-byte
+ * aligned (scale: 8); the arrays of one call must not overlap each other.
+ * Errors: INVALID_ARG (bad cfg, t < 1, n_tensors < 0, a NULL pointer, a bad type or multiplier),
+ * ALIGNMENT, UNSUPPORTED_SHAPE (over 2^31 tiles of 2048 elements), CUDA; nothing is launched if any tensor is refused. */
+poetx_status poetx_adamw_multi_step(const poetx_adamw_cfg* cfg, int n_tensors, const poetx_adamw_tensor* tensors,
+                                    int t, unsigned long long seed, poetx_stream stream);
+
 /* Host check of a permutation (HOST memory): POETX_OK if perm holds every value of [0, n)
  * exactly once, else POETX_ERR_INVALID_ARG.  The layer calls assume bijections and do not check
  * them; with the environment variable POETX_DEBUG set (and not "0") when the library first looks

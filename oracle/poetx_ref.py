@@ -37,6 +37,8 @@ __all__ = [
     "dense_transforms", "dense_weight", "forward_dense", "backward_dense", "cnp_grad",
     "forward_chain", "backward_chain", "backward_chain_G", "merge", "adamw_step", "train_schedule",
     "quantize_rows", "dequantize_rows", "xq_merge",
+    "element_bits", "e4m3_grid", "e4m3_values", "e4m3_moments", "bf16_stochastic",
+    "mx4_quantize", "mx4_dequantize", "mx4_merge",
 ]
 
 
@@ -381,3 +383,116 @@ def xq_merge(q, s, theta_R, theta_P, pi_L, pi_R, pi_L_new, pi_R_new, b, k):
     Wn, tR, tP = merge(dequantize_rows(q, s), theta_R, theta_P, pi_L, pi_R, pi_L_new, pi_R_new, b, k)
     qn, sn = quantize_rows(Wn)
     return Wn, qn, sn, tR, tP
+
+
+# ----------------------------------------------------------------- AdamW moments in 8 bits (e4m3)
+# 256 consecutive elements of a tensor share u = max|x| / 448 (x: the first moment, or the root of
+# the second), and each holds x / u on the e4m3 grid: 3 mantissa bits from 2^-6 to 448, multiples of
+# 2^-9 below.  Rounding is to nearest (ties to even), or up with the probability of the part cut off.
+def element_bits(n, tensor, seed):
+    """32 random bits of elements 0..n-1 of the tensor at position `tensor`: two rounds of
+    multiply and xor-shift, in integers modulo 2^32."""
+    M = 0xFFFFFFFF
+    salt = ((seed & M) + ((seed >> 32) & M) * 0x3C6EF373 + (tensor + 1) * 0xBB67AE85) & M
+    i = np.arange(n, dtype=np.uint64)
+    m32 = np.uint64(M)
+    h = ((i & m32) * np.uint64(0x9E3779B1) + np.uint64(salt) + (i >> np.uint64(32)) * np.uint64(0x6A09E667)) & m32
+    h = ((h ^ (h >> np.uint64(16))) * np.uint64(0x6A09E667)) & m32
+    h = ((h ^ (h >> np.uint64(15))) * np.uint64(0xBB67AE85)) & m32
+    return h ^ (h >> np.uint64(16))
+
+
+def e4m3_grid(a):
+    """Distance between e4m3 neighbours at |a| (a in (0, 448])."""
+    return np.exp2(np.floor(np.log2(np.maximum(np.abs(a), 2.0 ** -6))) - 3)
+
+
+def e4m3_values():
+    """The value of each of the 256 codes: sign, 4 exponent bits (bias 7), 3 mantissa bits; no
+    infinities, 0x7F and 0xFF are NaN."""
+    c = np.arange(256)
+    e, f = (c >> 3) & 15, c & 7
+    v = np.where(e == 0, f * 2.0 ** -9, (1 + f / 8) * 2.0 ** (e - 7.0))
+    v = np.where((c & 127) == 127, np.nan, v)
+    return np.where(c >= 128, -v, v)
+
+
+def e4m3_moments(x, positive, rnd16=None):
+    """(values on the grid, u per block of 256) of x [n]; `positive`: the root of a second moment,
+    where a positive value is never stored as 0.  rnd16: 16 random bits per element, or nearest."""
+    x = np.asarray(x, np.float64)
+    n = x.size
+    nb = (n + 255) // 256
+    pad = np.zeros(nb * 256)
+    pad[:n] = x
+    fine = np.isfinite(pad)
+    top = np.where(fine, np.abs(pad), 0).reshape(nb, 256).max(axis=1)
+    top = np.where(top < 2.0 ** -100, 0.0, top)
+    inv = np.repeat(np.where(top > 0, 448 / np.where(top > 0, top, 1), 0.0), 256)[:n]
+    ax = np.where(fine[:n], np.abs(x), 0)
+    a = np.minimum(ax * inv, 448)
+    g = e4m3_grid(a)
+    k = a / g
+    q = np.minimum((np.rint(k) if rnd16 is None else np.floor(k + rnd16 / 65536.0)) * g, 448)
+    if positive:
+        q = np.where(ax > 0, np.maximum(q, 2.0 ** -9), q)
+    q = np.where(x < 0, -q, q)
+    return np.where(fine[:n], q, np.nan), top / 448
+
+
+def bf16_stochastic(p, h):
+    """p on the bf16 grid (8 significant bits), up with the probability of the part cut off: the
+    random bits are the top 16 of the element's bits times the last multiplier."""
+    p = np.asarray(p, np.float64)
+    rnd = ((h * np.uint64(0xBB67AE85)) & np.uint64(0xFFFFFFFF)) >> np.uint64(16)
+    a = np.maximum(np.abs(p), 2.0 ** -126)
+    g = np.exp2(np.floor(np.log2(a)) - 7)
+    return np.sign(p) * np.floor(np.abs(p) / g + rnd / 65536.0) * g
+
+
+# ------------------------------------------------------------- MX4: a 4-bit resident W0'
+# The OCP microscaling format MXFP4: e2m1 codes (0, 1/2, 1, 3/2, 2, 3, 4, 6 with a sign) and one
+# power-of-two scale for 32 consecutive columns of a row, stored as its exponent plus 127 (E8M0;
+# 255 is NaN).  Scale exponent: floor(log2 absmax) - 2, the exponent of the largest code being 2;
+# values beyond 6 scales saturate.  Every step is exact, so the codes are a function of the input.
+_E2M1 = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def mx4_quantize(W):
+    """W [rows, cols], cols % 32 == 0 -> (codes uint8 [rows, cols/2], low nibble the even column;
+    scales uint8 [rows, cols/32])."""
+    W = np.asarray(W, np.float64)
+    rows, cols = W.shape
+    w = W.reshape(rows, cols // 32, 32)
+    fine = np.isfinite(w).all(axis=2)
+    amax = np.where(fine, np.abs(np.where(np.isfinite(w), w, 0)).max(axis=2), 1.0)
+    _, ex = np.frexp(amax)                       # amax = f 2^ex, 1/2 <= f < 1
+    e = np.where(amax > 0, np.clip(ex - 3, -127, 127), -127)
+    y = np.abs(np.where(np.isfinite(w), w, 0)) * np.exp2(-e.astype(np.float64))[:, :, None]
+    d = np.abs(y[..., None] - _E2M1)
+    code = np.argmin(d, axis=-1)                 # nearest; of two as near, the lower one ...
+    up = np.minimum(code + 1, 7)
+    tie = (d[np.arange(rows)[:, None, None], np.arange(cols // 32)[None, :, None], np.arange(32)[None, None, :], up]
+           == d.min(axis=-1)) & (up != code)
+    code = np.where(tie & (code % 2 == 1), up, code)  # ... unless the upper one is even
+    code = np.where(fine[:, :, None], code + 8 * np.signbit(w), 0).reshape(rows, cols).astype(np.uint8)
+    scales = np.where(fine, e + 127, 255).astype(np.uint8)
+    return code[:, 0::2] | (code[:, 1::2] << 4), scales
+
+
+def mx4_dequantize(codes, scales):
+    """The weight [rows, cols] that codes and scales stand for (float64)."""
+    codes, scales = np.asarray(codes), np.asarray(scales)
+    rows = codes.shape[0]
+    c = np.stack([codes & 15, codes >> 4], axis=2).reshape(rows, -1)
+    v = np.where(c >= 8, -1.0, 1.0) * _E2M1[c & 7]
+    s = np.where(scales == 255, np.nan, np.exp2(scales.astype(np.float64) - 127))
+    return (v.reshape(rows, -1, 32) * s[:, :, None]).reshape(rows, -1)
+
+
+def mx4_merge(codes, scales, theta_R, theta_P, pi_L, pi_R, pi_L_new, pi_R_new, b, k):
+    """Merge of the layer on an MX4 weight: the POET-X merge of the weight it stands for, then the
+    new W0' quantised again.  Returns (W0'_new before quantisation, codes, scales, theta_R, theta_P)."""
+    Wn, tR, tP = merge(mx4_dequantize(codes, scales), theta_R, theta_P, pi_L, pi_R, pi_L_new, pi_R_new, b, k)
+    cn, sn = mx4_quantize(Wn)
+    return Wn, cn, sn, tR, tP

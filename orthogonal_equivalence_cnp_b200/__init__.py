@@ -22,10 +22,13 @@ __all__ = [
     "poetx_xq_quantize", "poetx_xq_dequantize", "poetx_xq_forward", "poetx_xq_backward", "poetx_xq_merge",
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
+    "poetx_adamw_tensor", "poetx_adamw_multi_step", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
 ]
 
 POETX_F32, POETX_BF16 = 0, 1
 POETX_FAST, POETX_MEM = 0, 1
+POETX_MOMENT_F32, POETX_MOMENT_E4M3 = 0, 1
+POETX_MOMENT_BLOCK = 256
 STATUS = {
     0: "POETX_OK", 1: "POETX_ERR_INVALID_ARG", 2: "POETX_ERR_UNSUPPORTED_SHAPE", 3: "POETX_ERR_ALIGNMENT",
     4: "POETX_ERR_WORKSPACE", 5: "POETX_ERR_CUDA", 6: "POETX_ERR_DEVICE_TIMEOUT",
@@ -55,6 +58,13 @@ class poetx_adamw_cfg(ctypes.Structure):
                 ("beta2", ctypes.c_float), ("eps", ctypes.c_float), ("weight_decay", ctypes.c_float)]
 
 
+class poetx_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("scale", ctypes.c_void_p), ("n", ctypes.c_longlong), ("lr_scale", ctypes.c_float),
+                ("decay_scale", ctypes.c_float), ("param_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+                ("moment", ctypes.c_int)]
+
+
 class PoetxError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
@@ -80,6 +90,8 @@ _SIGNATURES = {
     "poetx_merge": (_I, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_adamw_step": (_I, [ctypes.POINTER(poetx_adamw_cfg), _LL, _I, _P, _P, _P, _P, _P]),
     "poetx_adamw_reset": (_I, [_LL, _P, _P, _P]),
+    "poetx_adamw_multi_step": (_I, [ctypes.POINTER(poetx_adamw_cfg), _I, ctypes.POINTER(poetx_adamw_tensor), _I,
+                                    ctypes.c_ulonglong, _P]),
     "poetx_wc_saved_size": (_SZ, [_D]),
     "poetx_wc_workspace_size": (_SZ, [_D]),
     "poetx_wc_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -275,6 +287,14 @@ def poetx_adamw_step(cfg, n, t, theta, grad, m, v, stream=None):
 
 def poetx_adamw_reset(n, m, v, stream=None):
     _check(lib().poetx_adamw_reset(n, _ptr(m), _ptr(v), _stream(stream)), "poetx_adamw_reset")
+
+
+def poetx_adamw_multi_step(cfg, n_tensors, tensors, t, seed=0, stream=None):
+    """tensors: a ctypes array of poetx_adamw_tensor (raw device addresses; optim.MultiAdamW builds one from
+    torch tensors and checks them)."""
+    if n_tensors > len(tensors):
+        raise ValueError(f"n_tensors = {n_tensors} exceeds the array's {len(tensors)} entries")
+    _check(lib().poetx_adamw_multi_step(cfg, n_tensors, tensors, t, seed, _stream(stream)), "poetx_adamw_multi_step")
 
 
 def poetx_wc_saved_size(desc) -> int:

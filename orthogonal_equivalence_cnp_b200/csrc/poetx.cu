@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "elementwise.cuh"
 #include "gemm.cuh"
+#include "optim.cuh"
 #include "sm100.cuh"
 #include "cnp_onchip.cuh"
 
@@ -1108,12 +1109,14 @@ poetx_status noalloc_scratch(char** out) {
 // =============================================================================== C ABI
 extern "C" {
 
+static bool adamw_cfg_ok(const poetx_adamw_cfg* cfg) {
+  return cfg != nullptr && cfg->lr >= 0.f && cfg->gamma >= 0.f && cfg->beta1 >= 0.f && cfg->beta1 < 1.f &&
+         cfg->beta2 >= 0.f && cfg->beta2 < 1.f && cfg->eps > 0.f && cfg->weight_decay >= 0.f;
+}
+
 poetx_status poetx_adamw_step(const poetx_adamw_cfg* cfg, long long n, int t, float* theta, const float* grad,
                               float* m, float* v, poetx_stream stream) {
-  if (cfg == nullptr || n < 0 || t < 1) return POETX_ERR_INVALID_ARG;
-  if (!(cfg->lr >= 0.f) || !(cfg->gamma >= 0.f) || !(cfg->beta1 >= 0.f && cfg->beta1 < 1.f) ||
-      !(cfg->beta2 >= 0.f && cfg->beta2 < 1.f) || !(cfg->eps > 0.f) || !(cfg->weight_decay >= 0.f))
-    return POETX_ERR_INVALID_ARG;
+  if (!adamw_cfg_ok(cfg) || n < 0 || t < 1) return POETX_ERR_INVALID_ARG;
   if (n == 0) return POETX_OK;
   POETX_TRY(check_ptrs({theta, grad, m, v}));
   const double bc1 = 1.0 - std::pow((double)cfg->beta1, (double)t);
@@ -1138,6 +1141,93 @@ poetx_status poetx_adamw_reset(long long n, float* m, float* v, poetx_stream str
   POETX_TRY(check_ptrs({m, v}));
   if (cudaMemsetAsync(m, 0, (size_t)n * 4, stream) != cudaSuccess) return POETX_ERR_CUDA;
   return cudaMemsetAsync(v, 0, (size_t)n * 4, stream) == cudaSuccess ? POETX_OK : POETX_ERR_CUDA;
+}
+
+}  // extern "C"
+
+template <int MAX>
+static poetx_status adamw_multi_launch(const poetx_adamw_cfg* cfg, const MultiCfg& c, int n_tensors,
+                                       const poetx_adamw_tensor* tensors, unsigned long long seed, cudaStream_t st) {
+  const uint32_t seed_salt = (uint32_t)seed + (uint32_t)(seed >> 32) * 0x3C6EF373u;
+  MultiArgs<MAX> a;
+  a.c = c;
+  for (int i = 0; i < n_tensors;) {
+    a.c.count = 0;
+    a.c.tiles = 0;
+    for (; i < n_tensors && a.c.count < MAX; ++i) {
+      const poetx_adamw_tensor& x = tensors[i];
+      if (x.n == 0) continue;
+      MultiTensor& d = a.t[a.c.count];
+      d.p = x.param; d.g = x.grad; d.m = x.m; d.v = x.v;
+      d.scale = reinterpret_cast<float2*>(x.scale);
+      d.n = (long)x.n;
+      d.eta = cfg->gamma * cfg->lr * x.lr_scale;
+      d.decay = cfg->weight_decay * x.decay_scale;
+      d.salt = seed_salt + ((uint32_t)i + 1u) * 0xBB67AE85u;
+      d.flags = (x.param_dtype == POETX_BF16 ? 1u : 0u) | (x.grad_dtype == POETX_BF16 ? 2u : 0u) |
+                (x.moment == POETX_MOMENT_E4M3 ? 4u : 0u);
+      a.first[a.c.count++] = a.c.tiles;
+      a.c.tiles += (uint32_t)((x.n + kMultiTile - 1) / kMultiTile);
+    }
+    if (a.c.count == 0) break;
+    auto kern = adamw_multi_kernel<MAX>;
+    int per_sm = 1;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMultiThreads, 0) != cudaSuccess)
+      return POETX_ERR_CUDA;
+    const uint32_t grid = std::min<uint32_t>(a.c.tiles, (uint32_t)(device_sms() * std::max(per_sm, 1)));
+    cudaLaunchConfig_t lc = {};
+    lc.gridDim = dim3(grid);
+    lc.blockDim = dim3(kMultiThreads);
+    lc.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    lc.attrs = attr;
+    lc.numAttrs = 1;
+    void* params[1] = {&a};  // the table is copied once, by the launch
+    LaunchScope ls(POETX_KC_OPTIMIZER, st);
+    if (cudaLaunchKernelExC(&lc, reinterpret_cast<const void*>(kern), params) != cudaSuccess) return POETX_ERR_CUDA;
+    POETX_TRY(last_launch());
+  }
+  return POETX_OK;
+}
+
+extern "C" {
+
+poetx_status poetx_adamw_multi_step(const poetx_adamw_cfg* cfg, int n_tensors, const poetx_adamw_tensor* tensors,
+                                    int t, unsigned long long seed, poetx_stream stream) {
+  if (!adamw_cfg_ok(cfg) || t < 1 || n_tensors < 0 || (n_tensors > 0 && tensors == nullptr))
+    return POETX_ERR_INVALID_ARG;
+  long long tiles = 0;
+  for (int i = 0; i < n_tensors; ++i) {
+    const poetx_adamw_tensor& x = tensors[i];
+    if (x.n < 0 || !(x.lr_scale >= 0.f) || !(x.decay_scale >= 0.f)) return POETX_ERR_INVALID_ARG;
+    if ((x.param_dtype != POETX_F32 && x.param_dtype != POETX_BF16) ||
+        (x.grad_dtype != POETX_F32 && x.grad_dtype != POETX_BF16) ||
+        (x.moment != POETX_MOMENT_F32 && x.moment != POETX_MOMENT_E4M3))
+      return POETX_ERR_INVALID_ARG;
+    if (x.n == 0) continue;
+    POETX_TRY(check_ptrs({x.param, x.grad, x.m, x.v}));
+    if (x.moment == POETX_MOMENT_E4M3) {
+      if (x.scale == nullptr) return POETX_ERR_INVALID_ARG;
+      if (reinterpret_cast<uintptr_t>(x.scale) & 7u) return POETX_ERR_ALIGNMENT;
+    }
+    if (x.n > (1LL << 42)) return POETX_ERR_UNSUPPORTED_SHAPE;
+    tiles += (x.n + kMultiTile - 1) / kMultiTile;
+    if (tiles > (1LL << 31)) return POETX_ERR_UNSUPPORTED_SHAPE;
+  }
+  const double bc1 = 1.0 - std::pow((double)cfg->beta1, (double)t);
+  const double bc2 = 1.0 - std::pow((double)cfg->beta2, (double)t);
+  MultiCfg c;
+  c.beta1 = cfg->beta1; c.beta2 = cfg->beta2;
+  c.inv_bc1 = (float)(1.0 / bc1);
+  c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
+  c.eps = cfg->eps;
+  c.stochastic = seed != 0;
+  c.count = 0;
+  c.tiles = 0;
+  if (n_tensors <= kMultiFew) return adamw_multi_launch<kMultiFew>(cfg, c, n_tensors, tensors, seed, stream);
+  return adamw_multi_launch<kMultiMany>(cfg, c, n_tensors, tensors, seed, stream);
 }
 
 poetx_status poetx_check_permutation(const int32_t* perm, int n) {
