@@ -49,74 +49,92 @@ static_assert(sizeof(MultiArgs<kMultiMany>) <= 32764, "the largest kernel argume
 // 32 random bits of element i of a tensor: two rounds of multiply and xor-shift over the element's
 // number and the tensor's salt (odd multipliers: fractional bits of the golden ratio, sqrt 2 and
 // sqrt 3).  A pure function of (seed, tensor, element), so a step is reproducible.
-__device__ __forceinline__ uint32_t element_bits(long i, uint32_t salt) {
-  uint32_t h = (uint32_t)i * 0x9E3779B1u + salt + (uint32_t)((unsigned long)i >> 32) * 0x6A09E667u;
+// i + e: element i is a multiple of four, so the upper half of the number does not change with e < 4.
+__device__ __forceinline__ uint32_t element_bits(long i, int e, uint32_t salt) {
+  uint32_t h = (uint32_t)i * 0x9E3779B1u + salt + (uint32_t)((unsigned long)i >> 32) * 0x6A09E667u +
+               (uint32_t)e * 0x9E3779B1u;
   h = (h ^ (h >> 16)) * 0x6A09E667u;
   h = (h ^ (h >> 15)) * 0xBB67AE85u;
   return h ^ (h >> 16);
 }
 
-// |y| <= 448 rounded to the e4m3 grid, up with the probability of the part that is cut off (16 random
-// bits; the bias is at most 2^-17 of a step).  From 2^-6 on the grid has 3 mantissa bits: the bits
-// below them are cut after the addition, which carries into the exponent where it should; under 2^-6 it
-// is the multiples of 2^-9.
+// 0 <= a <= 448 (or a rounding above) to the e4m3 grid, up with the probability of the part that is cut off (16
+// random bits; the bias is at most 2^-17 of a step).  From 2^-6 on the grid has 3 mantissa bits: the bits below
+// them are cut after the addition, which carries into the exponent where it should (beyond 448 the
+// conversion saturates).  Exact zero stays zero.
 __device__ __forceinline__ float e4m3_stochastic(float a, uint32_t rnd16) {
-  const float normal = __uint_as_float((__float_as_uint(a) + (rnd16 << 4)) & 0xFFF00000u);
-  const float small = floorf(__fadd_rn(a * 512.f, (float)rnd16 * (1.f / 65536.f))) * (1.f / 512.f);
-  return fminf(a < 0.015625f ? small : normal, 448.f);
+  return __uint_as_float((__float_as_uint(a) + (rnd16 << 4)) & 0xFFF00000u);
+}
+// The same under 2^-6, where the grid is the multiples of 2^-9: floor(512 a + rnd / 2^16), the floor by adding
+// 2^23 rounded down (exact for these sizes, and no slow conversion instruction).
+__device__ __forceinline__ float e4m3_stochastic_small(float a, uint32_t rnd16) {
+  const float r = __uint_as_float(0x3F800000u | (rnd16 << 7)) - 1.f;
+  return __fmaf_rn(__fadd_rd(__fmaf_rn(a, 512.f, r), 8388608.f), 0.001953125f, -16384.f);
 }
 
+// sqrt(v) rounded to nearest, without a branch: s = v y and h = y / 2 from the approximate y = 1 / sqrt(v), then one
+// correction s + (v - s^2) h in fused arithmetic (Markstein's final step).  Equal to __fsqrt_rn for every
+// float32 from 2^-100 up to the largest finite one (all of them compared: poetx_test_sqrt).
+constexpr float kSqrtLow = 7.888609052210118e-31f;  // 2^-100
+constexpr float kMaxFinite = 3.402823466e38f;
+__device__ __forceinline__ float sqrt_normal(float v) {
+  float y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
+  const float s = __fmul_rn(v, y);
+  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(0.5f, y), s);
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Four values of an fp32 or bf16 array at its element i; the last, partial block of a tensor is
+// read value by value, zeros past the end (a zero gradient and moment change nothing there).
 template <bool BF>
-__device__ __forceinline__ void load4(const void* base, long i, long n, float (&x)[4]) {
-  if (i + 4 <= n) {
-    if (BF) {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
-      x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-      x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xFFFF0000u);
-    } else {
-      const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
-      x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
-    }
+__device__ __forceinline__ void load4(const void* base, long i, float (&x)[4]) {
+  if (BF) {
+    const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(base) + i);
+    x[0] = __uint_as_float(u.x << 16); x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(u.y << 16); x[3] = __uint_as_float(u.y & 0xFFFF0000u);
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = i + e < n ? load_elem(base, i + e, BF ? BF16 : F32) : 0.f;
+    const float4 f = *reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    x[0] = f.x; x[1] = f.y; x[2] = f.z; x[3] = f.w;
   }
 }
-
+template <bool BF>
+__device__ __forceinline__ void load4_tail(const void* base, long i, long n, float (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) x[e] = i + e < n ? load_elem(base, i + e, BF ? BF16 : F32) : 0.f;
+}
 // bf16 results come in already on the bf16 grid or are rounded to nearest here.
 template <bool BF>
-__device__ __forceinline__ void store4(void* base, long i, long n, const float (&x)[4]) {
-  if (i + 4 <= n) {
-    if (BF) {
-      const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
-          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-    } else {
-      *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
-    }
+__device__ __forceinline__ void store4(void* base, long i, const float (&x)[4]) {
+  if (BF) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(base) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < n) store_elem(base, i + e, BF ? BF16 : F32, x[e]);
+    *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
-
-__device__ __forceinline__ uint32_t load4_codes(const uint8_t* c, long i, long n) {
-  if (i + 4 <= n) return *reinterpret_cast<const uint32_t*>(c + i);
+template <bool BF>
+__device__ __forceinline__ void store4_tail(void* base, long i, long n, const float (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) store_elem(base, i + e, BF ? BF16 : F32, x[e]);
+}
+__device__ __forceinline__ uint32_t codes4_tail(const uint8_t* c, long i, long n) {
   uint32_t w = 0;
 #pragma unroll
   for (int e = 0; e < 4; ++e)
     if (i + e < n) w |= (uint32_t)c[i + e] << (8 * e);
   return w;
 }
-__device__ __forceinline__ void store4_codes(uint8_t* c, long i, long n, uint32_t w) {
-  if (i + 4 <= n) {
-    *reinterpret_cast<uint32_t*>(c + i) = w;
-  } else {
+__device__ __forceinline__ void store_codes4_tail(uint8_t* c, long i, long n, uint32_t w) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (i + e < n) c[i + e] = (uint8_t)(w >> (8 * e));
-  }
+  for (int e = 0; e < 4; ++e)
+    if (i + e < n) c[i + e] = (uint8_t)(w >> (8 * e));
 }
 __device__ __forceinline__ void decode4(uint32_t w, float (&x)[4]) {
 #pragma unroll
@@ -133,129 +151,209 @@ __device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
   return lo | (hi << 16);
 }
 
-// Largest finite magnitude; a block whose largest is under 2^-100 is stored as zeros (448 / top would
-// overflow).
-__device__ __forceinline__ float warp_top(float top) {
+// Four codes of |x| * inv with x's sign; POSITIVE (the root of a second moment): a positive value
+// gets at least the smallest code, since m / (0 + eps) must not happen where gradients were seen.
+// Values under 2^-6 of the grid are rare (3.5e-5 of the block's largest), so they take a branch.
+template <bool POSITIVE>
+__device__ __forceinline__ uint32_t encode_moments(const float (&x)[4], float inv, bool stochastic,
+                                                   const uint32_t (&h)[4]) {
+  float q[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  return top < 7.888609052210118e-31f ? 0.f : top;
-}
-__device__ __forceinline__ float finite_abs(float x) {
-  const float a = fabsf(x);
-  return a <= 3.402823466e38f ? a : 0.f;  // NaN and infinity count as nothing
+  for (int e = 0; e < 4; ++e) q[e] = fabsf(__fmul_rn(x[e], inv));
+  if (stochastic) {
+    if (fminf(fminf(q[0], q[1]), fminf(q[2], q[3])) < 0.015625f) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const uint32_t r = POSITIVE ? h[e] >> 16 : h[e] & 0xFFFFu;
+        q[e] = q[e] < 0.015625f ? e4m3_stochastic_small(q[e], r) : e4m3_stochastic(q[e], r);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q[e] = e4m3_stochastic(q[e], POSITIVE ? h[e] >> 16 : h[e] & 0xFFFFu);
+    }
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    q[e] = POSITIVE ? (x[e] > 0.f ? fmaxf(q[e], 0.001953125f) : 0.f) : copysignf(q[e], x[e]);
+  return encode4(q);
 }
 
 // Eight elements of one thread: 4 at i0 and 4 at i0 + 128 of the warp's 256-element block.
 template <bool PBF, bool GBF, bool E4M3>
 __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg& a, long block, int lane) {
-  const long n = t.n, i0 = block * kMomentBlock + 4 * lane;
+  const long i0 = block * kMomentBlock + 4 * lane;
+  const bool full = (block + 1) * kMomentBlock <= t.n;
+  uint8_t* const cm = static_cast<uint8_t*>(t.m);
+  uint8_t* const cv = static_cast<uint8_t*>(t.v);
   float p[2][4], g[2][4], m[2][4], v[2][4];
+  uint32_t wm[2] = {0u, 0u}, wv[2] = {0u, 0u};
   float2 u = make_float2(0.f, 0.f);
+  if (full) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long i = i0 + 128 * h;
-    load4<PBF>(t.p, i, n, p[h]);
-    load4<GBF>(t.g, i, n, g[h]);
-    if (E4M3) {
-      const uint32_t cm = load4_codes(static_cast<const uint8_t*>(t.m), i, n);
-      const uint32_t cv = load4_codes(static_cast<const uint8_t*>(t.v), i, n);
-      decode4(cm, m[h]);
-      decode4(cv, v[h]);
-    } else {
-      load4<false>(t.m, i, n, m[h]);
-      load4<false>(t.v, i, n, v[h]);
+    for (int h = 0; h < 2; ++h) {
+      load4<PBF>(t.p, i0 + 128 * h, p[h]);
+      load4<GBF>(t.g, i0 + 128 * h, g[h]);
+      if (E4M3) {
+        wm[h] = *reinterpret_cast<const uint32_t*>(cm + i0 + 128 * h);
+        wv[h] = *reinterpret_cast<const uint32_t*>(cv + i0 + 128 * h);
+      } else {
+        load4<false>(t.m, i0 + 128 * h, m[h]);
+        load4<false>(t.v, i0 + 128 * h, v[h]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      load4_tail<PBF>(t.p, i0 + 128 * h, t.n, p[h]);
+      load4_tail<GBF>(t.g, i0 + 128 * h, t.n, g[h]);
+      if (E4M3) {
+        wm[h] = codes4_tail(cm, i0 + 128 * h, t.n);
+        wv[h] = codes4_tail(cv, i0 + 128 * h, t.n);
+      } else {
+        load4_tail<false>(t.m, i0 + 128 * h, t.n, m[h]);
+        load4_tail<false>(t.v, i0 + 128 * h, t.n, v[h]);
+      }
     }
   }
   if (E4M3) u = t.scale[block];
-  float top_m = 0.f, top_r = 0.f;
-  uint32_t rnd[2][4];
+  const bool stochastic = a.stochastic != 0;
+  const float shrink = t.eta * t.decay, rate = t.eta * a.inv_bc1;
+  // Largest magnitudes as integers, which order as the floats do and put infinities and NaN on top.
+  uint32_t top_m = 0u, top_r = 0u;
   // The moments take one rounding per operation (no contraction), so that the codes are a
   // function of the inputs that a float32 restatement reproduces bit for bit.
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
+  for (int h = 0; h < 2; ++h) {
+    if (E4M3) {
+      decode4(wm[h], m[h]);
+      decode4(wv[h], v[h]);
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float gg = g[h][e];
       float mm = m[h][e], vv = v[h][e];
       if (E4M3) {
         mm = __fmul_rn(mm, u.x);
         const float r0 = __fmul_rn(vv, u.y);
         vv = __fmul_rn(r0, r0);
       }
-      mm = __fadd_rn(__fmul_rn(a.beta1, mm), __fmul_rn(1.f - a.beta1, gg));
-      vv = __fadd_rn(__fmul_rn(a.beta2, vv), __fmul_rn(__fmul_rn(1.f - a.beta2, gg), gg));
-      const float r = __fsqrt_rn(vv);
-      const float denom = r * a.inv_sqrt_bc2 + a.eps;
+      m[h][e] = __fadd_rn(__fmul_rn(a.beta1, mm), __fmul_rn(1.f - a.beta1, g[h][e]));
+      v[h][e] = __fadd_rn(__fmul_rn(a.beta2, vv), __fmul_rn(__fmul_rn(1.f - a.beta2, g[h][e]), g[h][e]));
+    }
+    float r[4];
+    const float low = fminf(fminf(v[h][0], v[h][1]), fminf(v[h][2], v[h][3]));
+    const float high = fmaxf(fmaxf(v[h][0], v[h][1]), fmaxf(v[h][2], v[h][3]));
+    if (low >= kSqrtLow && high <= kMaxFinite) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = sqrt_normal(v[h][e]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = __fsqrt_rn(v[h][e]);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float up = m[h][e] * rate * rcp_approx(__fmaf_rn(r[e], a.inv_sqrt_bc2, a.eps));
       float th = p[h][e];
-      th = th - t.eta * (t.decay * th + __fdividef(mm * a.inv_bc1, denom));
-      m[h][e] = mm;
-      v[h][e] = E4M3 ? r : vv;
-      if (a.stochastic && (E4M3 || PBF)) rnd[h][e] = element_bits(i0 + 128 * h + e, t.salt);
-      if (PBF && a.stochastic) {
-        const uint32_t b = __float_as_uint(th);
-        if ((b & 0x7F800000u) != 0x7F800000u)
-          th = __uint_as_float((b + ((rnd[h][e] * 0xBB67AE85u) >> 16)) & 0xFFFF0000u);
+      th = __fsub_rn(th, __fmaf_rn(shrink, th, up));
+      if (PBF && stochastic && th == th) {  // an infinity keeps its bits under this addition
+        const uint32_t b = element_bits(i0 + 128 * h, e, t.salt) * 0xBB67AE85u;
+        th = __uint_as_float((__float_as_uint(th) + (b >> 16)) & 0xFFFF0000u);
       }
       p[h][e] = th;
       if (E4M3) {
-        top_m = fmaxf(top_m, finite_abs(mm));
-        top_r = fmaxf(top_r, finite_abs(r));
+        v[h][e] = r[e];
+        top_m = max(top_m, __float_as_uint(fabsf(m[h][e])));
+        top_r = max(top_r, __float_as_uint(r[e]));
       }
     }
+  }
+  if (full) {
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const long i = i0 + 128 * h;
-    store4<PBF>(t.p, i, n, p[h]);
-    if (!E4M3) {
-      store4<false>(t.m, i, n, m[h]);
-      store4<false>(t.v, i, n, v[h]);
+    for (int h = 0; h < 2; ++h) {
+      store4<PBF>(t.p, i0 + 128 * h, p[h]);
+      if (!E4M3) {
+        store4<false>(t.m, i0 + 128 * h, m[h]);
+        store4<false>(t.v, i0 + 128 * h, v[h]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      store4_tail<PBF>(t.p, i0 + 128 * h, t.n, p[h]);
+      if (!E4M3) {
+        store4_tail<false>(t.m, i0 + 128 * h, t.n, m[h]);
+        store4_tail<false>(t.v, i0 + 128 * h, t.n, v[h]);
+      }
     }
   }
   if (!E4M3) return;
-  top_m = warp_top(top_m);
-  top_r = warp_top(top_r);
-  const float inv_m = top_m > 0.f ? __fdiv_rn(448.f, top_m) : 0.f;
-  const float inv_r = top_r > 0.f ? __fdiv_rn(448.f, top_r) : 0.f;
+  top_m = __reduce_max_sync(0xffffffffu, top_m);
+  top_r = __reduce_max_sync(0xffffffffu, top_r);
+  uint32_t bad_m[2] = {0u, 0u}, bad_r[2] = {0u, 0u};
+  if (max(top_m, top_r) >= 0x7F800000u) {
+    // A NaN or an infinity is left out of the block's maximum and stored as the NaN code.
+    top_m = top_r = 0u;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        if (!(fabsf(m[h][e]) <= kMaxFinite)) { bad_m[h] |= 0x7Fu << (8 * e); m[h][e] = 0.f; }
+        if (!(v[h][e] <= kMaxFinite)) { bad_r[h] |= 0x7Fu << (8 * e); v[h][e] = 0.f; }
+        top_m = max(top_m, __float_as_uint(fabsf(m[h][e])));
+        top_r = max(top_r, __float_as_uint(v[h][e]));
+      }
+    top_m = __reduce_max_sync(0xffffffffu, top_m);
+    top_r = __reduce_max_sync(0xffffffffu, top_r);
+  }
+  // A block whose largest is under 2^-100 is stored as zeros (448 / top would overflow).
+  const float tm = __uint_as_float(top_m) < kSqrtLow ? 0.f : __uint_as_float(top_m);
+  const float tr = __uint_as_float(top_r) < kSqrtLow ? 0.f : __uint_as_float(top_r);
+  const float inv_m = tm > 0.f ? __fmul_rn(448.f, __frcp_rn(tm)) : 0.f;
+  const float inv_r = tr > 0.f ? __fmul_rn(448.f, __frcp_rn(tr)) : 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    float qm[4], qr[4];
+    uint32_t rnd[4] = {0u, 0u, 0u, 0u};
+    if (stochastic) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = m[h][e], r = v[h][e];
-      float am = fminf(fabsf(__fmul_rn(x, inv_m)), 448.f), ar = fminf(__fmul_rn(r, inv_r), 448.f);
-      if (a.stochastic) {
-        am = e4m3_stochastic(am, rnd[h][e] & 0xFFFFu);
-        ar = e4m3_stochastic(ar, rnd[h][e] >> 16);
-      }
-      // The smallest code stands in for a second moment that would round to zero: m / (0 + eps) must
-      // not happen where gradients were seen.
-      if (r > 0.f) ar = fmaxf(ar, 0.001953125f);
-      const float nan = __uint_as_float(0x7FC00000u);
-      qm[e] = fabsf(x) <= 3.402823466e38f ? copysignf(am, x) : nan;
-      qr[e] = r <= 3.402823466e38f ? ar : nan;
+      for (int e = 0; e < 4; ++e) rnd[e] = element_bits(i0 + 128 * h, e, t.salt);
     }
-    store4_codes(static_cast<uint8_t*>(t.m), i0 + 128 * h, n, encode4(qm));
-    store4_codes(static_cast<uint8_t*>(t.v), i0 + 128 * h, n, encode4(qr));
+    wm[h] = encode_moments<false>(m[h], inv_m, stochastic, rnd) | bad_m[h];
+    wv[h] = encode_moments<true>(v[h], inv_r, stochastic, rnd) | bad_r[h];
   }
-  if (lane == 0) t.scale[block] = make_float2(__fdiv_rn(top_m, 448.f), __fdiv_rn(top_r, 448.f));
+  if (full) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      *reinterpret_cast<uint32_t*>(cm + i0 + 128 * h) = wm[h];
+      *reinterpret_cast<uint32_t*>(cv + i0 + 128 * h) = wv[h];
+    }
+  } else {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      store_codes4_tail(cm, i0 + 128 * h, t.n, wm[h]);
+      store_codes4_tail(cv, i0 + 128 * h, t.n, wv[h]);
+    }
+  }
+  if (lane == 0) t.scale[block] = make_float2(__fmul_rn(tm, 1.f / 448.f), __fmul_rn(tr, 1.f / 448.f));
 }
 
-// Tiles of 2048 elements (eight 256-element blocks, one per warp) over all tensors; a block of threads
-// takes every gridDim-th tile and finds its tensor by bisection in the table, which sits in constant
-// memory because it is a kernel argument: nothing is uploaded, and a captured launch keeps its own copy.
+// Tiles of 2048 elements (eight 256-element blocks, one per warp) over all tensors.  Each block of threads
+// takes a run of consecutive tiles: it finds the first one's tensor by bisection in the table and walks on from
+// there.  The table is a kernel argument (constant memory): nothing is uploaded, and a captured launch keeps its own.
 template <int MAX>
-__global__ void __launch_bounds__(kMultiThreads) adamw_multi_kernel(const __grid_constant__ MultiArgs<MAX> args) {
+__global__ void __launch_bounds__(kMultiThreads, 4) adamw_multi_kernel(const __grid_constant__ MultiArgs<MAX> args) {
   sm100::griddep_wait();
   const MultiCfg& a = args.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  for (uint32_t tile = blockIdx.x; tile < a.tiles; tile += gridDim.x) {
-    int lo = 0, hi = a.count - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (args.first[mid] <= tile) lo = mid; else hi = mid - 1;
-    }
-    const MultiTensor& t = args.t[lo];
-    const long block = (long)(tile - args.first[lo]) * (kMultiTile / kMomentBlock) + warp;
+  uint32_t tile = (uint32_t)((unsigned long)a.tiles * blockIdx.x / gridDim.x);
+  const uint32_t end = (uint32_t)((unsigned long)a.tiles * (blockIdx.x + 1) / gridDim.x);
+  int at = 0, hi = a.count - 1;
+  while (at < hi) {
+    const int mid = (at + hi + 1) >> 1;
+    if (args.first[mid] <= tile) at = mid; else hi = mid - 1;
+  }
+  for (; tile < end; ++tile) {
+    if (at + 1 < a.count && tile >= args.first[at + 1]) ++at;  // every listed tensor has a tile
+    const MultiTensor& t = args.t[at];
+    const long block = (long)(tile - args.first[at]) * (kMultiTile / kMomentBlock) + warp;
     if (block * kMomentBlock >= t.n) continue;  // past the tensor's last block (the whole warp)
     switch (t.flags) {
       case 0: adamw_block<false, false, false>(t, a, block, lane); break;
