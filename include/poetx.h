@@ -316,7 +316,8 @@ poetx_status poetx_adamw_reset(long long n, float* m, float* v, poetx_stream str
  * POETX_MOMENT_E4M3: POETX_MOMENT_BLOCK = 256 consecutive elements of the tensor (the last block may be
  *   shorter) share scale[block] = {u_m, u_r} with u_m = max |m| / 448 and u_r = max r / 448; m and v hold one
  *   e4m3 code per element (uint8 [n]; float8_e4m3fn of other libraries) with m = u_m * code(m) and
- *   sqrt(v) = u_r * code(v).  All-zero codes and scales are the moments' start.  The step uses the moments
+ *   sqrt(v) = u_r * code(v).  Before rounding to a code, m and r are multiplied by 448 * (1 / max), and
+ *   u = max * (1 / 448), each operation rounded to float32.  All-zero codes and scales are the moments' start.  The step uses the moments
  *   before they are rounded; r > 0 is never stored as 0 (at least 2^-9 u_r), so an element whose
  *   gradients were seen is never divided by eps alone.  A block whose largest |m| is under 2^-100 stores
  *   zeros; a NaN or infinite moment is stored as NaN and left out of its block's maximum.

@@ -44,6 +44,11 @@ poetx_status poetx_test_gemm(int dtype, int M, int N, int K, int batch, int spli
  * ALIGNMENT, CUDA. */
 poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_stream stream);
 
+/* Compares the square root of the 8-bit moments with CUDA's correctly rounded one for the float32 numbers with the
+ * bit patterns first..last, all from 2^-100 (0x0D800000) up to the largest finite one (0x7F7FFFFF);
+ * *mismatches (device memory, 8-byte aligned) receives how many differ. */
+poetx_status poetx_test_sqrt(unsigned first, unsigned last, unsigned long long* mismatches, poetx_stream stream);
+
 #ifdef __cplusplus
 }
 #endif

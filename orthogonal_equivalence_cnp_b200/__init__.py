@@ -22,7 +22,7 @@ __all__ = [
     "poetx_xq_quantize", "poetx_xq_dequantize", "poetx_xq_forward", "poetx_xq_backward", "poetx_xq_merge",
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
-    "poetx_adamw_tensor", "poetx_adamw_multi_step", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
+    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
 ]
 
 POETX_F32, POETX_BF16 = 0, 1
@@ -106,6 +106,7 @@ _SIGNATURES = {
     "poetx_fourperm_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_fourperm_backward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_test_wait_timeout": (_I, [_LL, _P, _P]),
+    "poetx_test_sqrt": (_I, [ctypes.c_uint, ctypes.c_uint, _P, _P]),
     "poetx_status_string": (ctypes.c_char_p, [_I]),
     "poetx_device_status": (_I, [ctypes.POINTER(ctypes.c_int)]),
     "poetx_launch_count": (ctypes.c_ulonglong, []),
@@ -426,6 +427,11 @@ def poetx_cnp_blocks_noalloc(desc, n_blocks, theta, Q, stream=None):
 
 def poetx_test_wait_timeout(limit_ns, returned, stream=None):
     _check(lib().poetx_test_wait_timeout(int(limit_ns), _ptr(returned), _stream(stream)), "poetx_test_wait_timeout")
+
+
+def poetx_test_sqrt(first, last, mismatches, stream=None):
+    _need(mismatches, "mismatches", 1)
+    _check(lib().poetx_test_sqrt(first, last, _ptr(mismatches), _stream(stream)), "poetx_test_sqrt")
 
 
 def poetx_fourperm_workspace_size(desc, n_tokens):

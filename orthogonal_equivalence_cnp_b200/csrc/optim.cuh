@@ -34,7 +34,7 @@ struct MultiTensor {
   uint32_t salt, flags;
 };
 struct MultiCfg {
-  float beta1, beta2, inv_bc1, inv_sqrt_bc2, eps;
+  float beta1, beta2, inv_bc1, inv_sqrt_bc2, eps, minus_zero;
   int count;
   uint32_t stochastic, tiles;
 };
@@ -46,17 +46,50 @@ struct MultiArgs {
 };
 static_assert(sizeof(MultiArgs<kMultiMany>) <= 32764, "the largest kernel argument");
 
-// 32 random bits of element i of a tensor: two rounds of multiply and xor-shift over the element's
-// number and the tensor's salt (odd multipliers: fractional bits of the golden ratio, sqrt 2 and
-// sqrt 3).  A pure function of (seed, tensor, element), so a step is reproducible.
-// i + e: element i is a multiple of four, so the upper half of the number does not change with e < 4.
+// 32 random bits of element i + e of a tensor (i a multiple of four, e < 4): two rounds of multiply and
+// xor-shift over the element's number and the tensor's salt (odd multipliers: fractional bits of the
+// golden ratio, sqrt 2 and sqrt 3), then h ^ (h >> 16), which element_finish adds.  A pure function of
+// (seed, tensor, element), so a step is reproducible.
 __device__ __forceinline__ uint32_t element_bits(long i, int e, uint32_t salt) {
   uint32_t h = (uint32_t)i * 0x9E3779B1u + salt + (uint32_t)((unsigned long)i >> 32) * 0x6A09E667u +
                (uint32_t)e * 0x9E3779B1u;
   h = (h ^ (h >> 16)) * 0x6A09E667u;
-  h = (h ^ (h >> 15)) * 0xBB67AE85u;
-  return h ^ (h >> 16);
+  return (h ^ (h >> 15)) * 0xBB67AE85u;
 }
+__device__ __forceinline__ uint32_t element_finish(uint32_t h) { return h ^ (h >> 16); }
+__device__ __forceinline__ uint32_t element_low16(uint32_t h) { return (h ^ (h >> 16)) & 0xFFFFu; }
+__device__ __forceinline__ uint32_t element_high16(uint32_t h) { return h >> 16; }
+
+// Pairs of floats in one 64-bit register: one instruction for two roundings (each as the scalar one).
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float lo, float hi) {
+  f32x2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ void unpair(f32x2 x, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+  f32x2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+  f32x2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f32x2 both(float x) { return pair(x, x); }
+// A product that keeps its own rounding.  The compiler merges a packed product into the packed sum that follows
+// it (one rounding instead of two) even where both say .rn, and sees through a constant zero; with a -0 that
+// it cannot know, a b + -0 is a b rounded, in the one instruction a product takes anyway.
+__device__ __forceinline__ f32x2 mul2_alone(f32x2 a, f32x2 b, float minus_zero) { return fma2(a, b, both(minus_zero)); }
 
 // 0 <= a <= 448 (or a rounding above) to the e4m3 grid, up with the probability of the part that is cut off (16
 // random bits; the bias is at most 2^-17 of a step).  From 2^-6 on the grid has 3 mantissa bits: the bits below
@@ -77,11 +110,17 @@ __device__ __forceinline__ float e4m3_stochastic_small(float a, uint32_t rnd16) 
 // float32 from 2^-100 up to the largest finite one (all of them compared: poetx_test_sqrt).
 constexpr float kSqrtLow = 7.888609052210118e-31f;  // 2^-100
 constexpr float kMaxFinite = 3.402823466e38f;
-__device__ __forceinline__ float sqrt_normal(float v) {
+__device__ __forceinline__ float rsqrt_approx(float v) {
   float y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v));
-  const float s = __fmul_rn(v, y);
-  return __fmaf_rn(__fmaf_rn(-s, s, v), __fmul_rn(0.5f, y), s);
+  return y;
+}
+__device__ __forceinline__ f32x2 sqrt2_normal(f32x2 v) {
+  float a, b;
+  unpair(v, a, b);
+  const f32x2 y = pair(rsqrt_approx(a), rsqrt_approx(b));
+  const f32x2 s = mul2(v, y);
+  return fma2(fma2(mul2(s, both(-1.f)), s, v), mul2(both(0.5f), y), s);
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -158,23 +197,28 @@ template <bool POSITIVE>
 __device__ __forceinline__ uint32_t encode_moments(const float (&x)[4], float inv, bool stochastic,
                                                    const uint32_t (&h)[4]) {
   float q[4];
+  unpair(mul2(pair(x[0], x[1]), both(inv)), q[0], q[1]);
+  unpair(mul2(pair(x[2], x[3]), both(inv)), q[2], q[3]);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = fabsf(__fmul_rn(x[e], inv));
+  for (int e = 0; e < 4; ++e) q[e] = fabsf(q[e]);
   if (stochastic) {
     if (fminf(fminf(q[0], q[1]), fminf(q[2], q[3])) < 0.015625f) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const uint32_t r = POSITIVE ? h[e] >> 16 : h[e] & 0xFFFFu;
+        const uint32_t r = POSITIVE ? element_high16(h[e]) : element_low16(h[e]);
         q[e] = q[e] < 0.015625f ? e4m3_stochastic_small(q[e], r) : e4m3_stochastic(q[e], r);
       }
     } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) q[e] = e4m3_stochastic(q[e], POSITIVE ? h[e] >> 16 : h[e] & 0xFFFFu);
+      for (int e = 0; e < 4; ++e)
+        q[e] = e4m3_stochastic(q[e], POSITIVE ? element_high16(h[e]) : element_low16(h[e]));
     }
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
-    q[e] = POSITIVE ? (x[e] > 0.f ? fmaxf(q[e], 0.001953125f) : 0.f) : copysignf(q[e], x[e]);
+  for (int e = 0; e < 4; ++e) {
+    if (!POSITIVE) q[e] = copysignf(q[e], x[e]);
+    else if (x[e] > 0.f) q[e] = fmaxf(q[e], 0.001953125f);
+  }
   return encode4(q);
 }
 
@@ -220,6 +264,7 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
   const float shrink = t.eta * t.decay, rate = t.eta * a.inv_bc1;
   // Largest magnitudes as integers, which order as the floats do and put infinities and NaN on top.
   uint32_t top_m = 0u, top_r = 0u;
+  uint32_t rnd[2][4] = {};
   // The moments take one rounding per operation (no contraction), so that the codes are a
   // function of the inputs that a float32 restatement reproduces bit for bit.
 #pragma unroll
@@ -228,37 +273,48 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
       decode4(wm[h], m[h]);
       decode4(wv[h], v[h]);
     }
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      float mm = m[h][e], vv = v[h][e];
-      if (E4M3) {
-        mm = __fmul_rn(mm, u.x);
-        const float r0 = __fmul_rn(vv, u.y);
-        vv = __fmul_rn(r0, r0);
-      }
-      m[h][e] = __fadd_rn(__fmul_rn(a.beta1, mm), __fmul_rn(1.f - a.beta1, g[h][e]));
-      v[h][e] = __fadd_rn(__fmul_rn(a.beta2, vv), __fmul_rn(__fmul_rn(1.f - a.beta2, g[h][e]), g[h][e]));
-    }
+    f32x2 r2[2], m2[2];
     float r[4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      f32x2 mm = pair(m[h][2 * q], m[h][2 * q + 1]), vv = pair(v[h][2 * q], v[h][2 * q + 1]);
+      const f32x2 gg = pair(g[h][2 * q], g[h][2 * q + 1]);
+      if (E4M3) {
+        mm = mul2(mm, both(u.x));
+        vv = mul2(vv, both(u.y));
+        vv = mul2(vv, vv);
+      }
+      m2[q] = add2(mul2_alone(both(a.beta1), mm, a.minus_zero), mul2_alone(both(1.f - a.beta1), gg, a.minus_zero));
+      r2[q] = add2(mul2_alone(both(a.beta2), vv, a.minus_zero),
+                   mul2_alone(mul2(both(1.f - a.beta2), gg), gg, a.minus_zero));
+      unpair(m2[q], m[h][2 * q], m[h][2 * q + 1]);
+      unpair(r2[q], v[h][2 * q], v[h][2 * q + 1]);
+    }
     const float low = fminf(fminf(v[h][0], v[h][1]), fminf(v[h][2], v[h][3]));
     const float high = fmaxf(fmaxf(v[h][0], v[h][1]), fmaxf(v[h][2], v[h][3]));
     if (low >= kSqrtLow && high <= kMaxFinite) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = sqrt_normal(v[h][e]);
+      r2[0] = sqrt2_normal(r2[0]);
+      r2[1] = sqrt2_normal(r2[1]);
     } else {
+      r2[0] = pair(__fsqrt_rn(v[h][0]), __fsqrt_rn(v[h][1]));
+      r2[1] = pair(__fsqrt_rn(v[h][2]), __fsqrt_rn(v[h][3]));
+    }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = __fsqrt_rn(v[h][e]);
+    for (int q = 0; q < 2; ++q) {
+      unpair(r2[q], r[2 * q], r[2 * q + 1]);
+      float d0, d1;
+      unpair(fma2(r2[q], both(a.inv_sqrt_bc2), both(a.eps)), d0, d1);
+      const f32x2 up = mul2(mul2(m2[q], both(rate)), pair(rcp_approx(d0), rcp_approx(d1)));
+      const f32x2 th = pair(p[h][2 * q], p[h][2 * q + 1]);
+      unpair(fma2(fma2(both(shrink), th, up), both(-1.f), th), p[h][2 * q], p[h][2 * q + 1]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float up = m[h][e] * rate * rcp_approx(__fmaf_rn(r[e], a.inv_sqrt_bc2, a.eps));
-      float th = p[h][e];
-      th = __fsub_rn(th, __fmaf_rn(shrink, th, up));
-      if (PBF && stochastic && th == th) {  // an infinity keeps its bits under this addition
-        const uint32_t b = element_bits(i0 + 128 * h, e, t.salt) * 0xBB67AE85u;
-        th = __uint_as_float((__float_as_uint(th) + (b >> 16)) & 0xFFFF0000u);
+      if (stochastic && (E4M3 || PBF)) rnd[h][e] = element_bits(i0 + 128 * h, e, t.salt);
+      if (PBF && stochastic && p[h][e] == p[h][e]) {  // an infinity keeps its bits under this addition
+        const uint32_t b = element_finish(rnd[h][e]) * 0xBB67AE85u;
+        p[h][e] = __uint_as_float((__float_as_uint(p[h][e]) + (b >> 16)) & 0xFFFF0000u);
       }
-      p[h][e] = th;
       if (E4M3) {
         v[h][e] = r[e];
         top_m = max(top_m, __float_as_uint(fabsf(m[h][e])));
@@ -311,13 +367,8 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
   const float inv_r = tr > 0.f ? __fmul_rn(448.f, __frcp_rn(tr)) : 0.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    uint32_t rnd[4] = {0u, 0u, 0u, 0u};
-    if (stochastic) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) rnd[e] = element_bits(i0 + 128 * h, e, t.salt);
-    }
-    wm[h] = encode_moments<false>(m[h], inv_m, stochastic, rnd) | bad_m[h];
-    wv[h] = encode_moments<true>(v[h], inv_r, stochastic, rnd) | bad_r[h];
+    wm[h] = encode_moments<false>(m[h], inv_m, stochastic, rnd[h]) | bad_m[h];
+    wv[h] = encode_moments<true>(v[h], inv_r, stochastic, rnd[h]) | bad_r[h];
   }
   if (full) {
 #pragma unroll

@@ -1222,7 +1222,8 @@ poetx_status poetx_adamw_multi_step(const poetx_adamw_cfg* cfg, int n_tensors, c
   c.beta1 = cfg->beta1; c.beta2 = cfg->beta2;
   c.inv_bc1 = (float)(1.0 / bc1);
   c.inv_sqrt_bc2 = (float)(1.0 / std::sqrt(bc2));
-  c.eps = cfg->eps;
+  c.eps = std::max(cfg->eps, 1.17549435e-38f);  // the kernel's reciprocal takes a subnormal number for zero
+  c.minus_zero = -0.f;
   c.stochastic = seed != 0;
   c.count = 0;
   c.tiles = 0;
@@ -1940,6 +1941,27 @@ poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_st
   if ((reinterpret_cast<uintptr_t>(returned) & 3u) != 0) return POETX_ERR_ALIGNMENT;
   LaunchScope ls(POETX_KC_ELEMENTWISE, stream);
   wait_probe_kernel<<<1, 32, 0, stream>>>((unsigned long long)limit_ns, returned);
+  return last_launch();
+}
+
+__global__ void sqrt_probe_kernel(unsigned first, unsigned last, unsigned long long* mismatches) {
+  const unsigned long long step = (unsigned long long)gridDim.x * blockDim.x;
+  unsigned bad = 0;
+  for (unsigned long long i = first + (unsigned long long)blockIdx.x * blockDim.x + threadIdx.x; i <= last; i += step) {
+    const float v = __uint_as_float((unsigned)i);
+    float r, unused;
+    unpair(sqrt2_normal(pair(v, 1.f)), r, unused);
+    bad += r != __fsqrt_rn(v);
+  }
+  if (bad) atomicAdd(mismatches, (unsigned long long)bad);
+}
+
+poetx_status poetx_test_sqrt(unsigned first, unsigned last, unsigned long long* mismatches, poetx_stream stream) {
+  if (mismatches == nullptr || first < 0x0D800000u || last > 0x7F7FFFFFu || first > last) return POETX_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(mismatches) & 7u) return POETX_ERR_ALIGNMENT;
+  if (cudaMemsetAsync(mismatches, 0, 8, stream) != cudaSuccess) return POETX_ERR_CUDA;
+  LaunchScope ls(POETX_KC_ELEMENTWISE, stream);
+  sqrt_probe_kernel<<<kNumSms * 8, 256, 0, stream>>>(first, last, mismatches);
   return last_launch();
 }
 

@@ -108,3 +108,10 @@ def test_new_moments():
         optim.new_moments(torch.zeros(7), "int8")
     with pytest.raises(ValueError):
         optim.MultiAdamW.from_params([torch.zeros(3)], [])
+
+
+def test_sqrt_probe_refusals():
+    L = P.lib()
+    assert L.poetx_test_sqrt(0x0D7FFFFF, 0x3F800000, A, None) == 1 and L.poetx_test_sqrt(0x3F800000, 0x7F800000, A, None) == 1
+    assert L.poetx_test_sqrt(2, 1, A, None) == 1 and L.poetx_test_sqrt(0x3F800000, 0x3F800000, None, None) == 1
+    assert L.poetx_test_sqrt(0x3F800000, 0x3F800000, A + 4, None) == 3

@@ -1,8 +1,11 @@
 """The many-tensor AdamW step against the oracle, with fp32 and e4m3 moments.
 
-Tolerances.  A float32 rounding is off by at most 2^-24 of the value (u below).  The moments take five
-roundings each and sqrt(v) one more (half of v's error): under 8u.  The parameter's update is their quotient
-with a fast division (2 ulp): under d = 32u of the update's own size plus 2u of the parameter.  A bf16 parameter
+Tolerances.  A float32 rounding is off by at most 2^-24 of the value (u below).  The first moment takes four (the
+decoded old one, two products, the sum): under 4u of beta1 |m| + (1 - beta1) |g|, which cancellation can make much
+larger than |m|'s own rounding; v takes five, all of one sign, and its root half of them and one: 3.5u.  The
+update is their quotient: the denominator 2u more, the approximate reciprocal 2u, the rate 2u, two products and
+the sum with the decay 3u: under 16u of `size`, the update with beta1 |m| + (1 - beta1) |g| in m's place.  The
+subtraction adds u of the parameter.  So d = 16u size + 2u |p|.  A bf16 parameter
 rounded to nearest is off by half a step of its grid (2^-8 of the value) and d.  Rounded stochastically, both
 sides add the same random part r and cut: for x and x' with |x - x'| <= d, cut(x + r) and cut(x' + r) differ by
 no more than d and one step (2^-7 of the value); where the parameter nearly cancels its update, d is the
@@ -56,10 +59,14 @@ def _expect(x, index, t, seed, lr_scale=1.0, decay_scale=1.0):
     if x.scale is not None:
         s = np.repeat(x.scale.cpu().numpy().astype(np.float64), 256, axis=0)[:p.size]
         m, v = m * s[:, 0], (v * s[:, 1]) ** 2
+    m0, v0 = m, v
     p1, m, v = O.adamw_step(p, g, m, v, t, F32["lr"] * lr_scale, F32["gamma"], F32["beta1"], F32["beta2"], F32["eps"],
                             F32["weight_decay"] * decay_scale)
+    size = np.abs(O.adamw_step(-np.abs(p), np.abs(g), np.abs(m0), v0, t, F32["lr"] * lr_scale, F32["gamma"],
+                               F32["beta1"], F32["beta2"], F32["eps"], 0.0)[0] + np.abs(p))
+    size = size + F32["lr"] * lr_scale * F32["gamma"] * F32["weight_decay"] * decay_scale * np.abs(p)
     h = O.element_bits(p.size, index, seed) if seed else None
-    out = dict(p=p1, up=p1 - p, p_bf=O.bf16_stochastic(p1, h) if seed else None)
+    out = dict(p=p1, d=16 * U * size + 2 * U * np.abs(p1), p_bf=O.bf16_stochastic(p1, h) if seed else None)
     if x.scale is None:
         return dict(out, m=m, v=v, scale=None)
     r = np.sqrt(v)
@@ -71,13 +78,12 @@ def _expect(x, index, t, seed, lr_scale=1.0, decay_scale=1.0):
 def _check(x, e, seed):
     p = to_np(x.param).ravel()
     if x.param.dtype == torch.float32:
-        assert np.all(np.abs(p - e["p"]) <= 32 * U * np.abs(e["up"]) + 2 * U * np.abs(e["p"]) + 1e-44)
+        assert np.all(np.abs(p - e["p"]) <= e["d"] + 1e-44)
     elif seed:
-        d = 32 * U * np.abs(e["up"]) + 2 * U * np.abs(e["p"])
-        assert np.all(np.abs(p - e["p_bf"]) <= d + 2.0 ** -7 * np.abs(e["p_bf"]) + 1e-38)
+        assert np.all(np.abs(p - e["p_bf"]) <= e["d"] + 2.0 ** -7 * np.abs(e["p_bf"]) + 1e-38)
         assert np.count_nonzero(p != e["p_bf"]) <= 5 + 4 * 2.0 ** -16 * p.size
     else:
-        assert np.all(np.abs(p - e["p"]) <= (2.0 ** -8 + 4 * U) * np.abs(e["p"]) + 32 * U * np.abs(e["up"]))
+        assert np.all(np.abs(p - e["p"]) <= 2.0 ** -8 * (np.abs(e["p"]) + e["d"]) + e["d"])
     if x.scale is None:
         assert np.all(np.abs(to_np(x.m) - e["m"]) <= 8 * U * (np.abs(e["m"]) + np.abs(to_np(x.grad).ravel())))
         assert np.all(np.abs(to_np(x.v) - e["v"]) <= 8 * U * e["v"] + 1e-44)
@@ -111,6 +117,33 @@ def test_one_step_of_many_sizes(moments, pdt, gdt, seed):
     for x, e in zip(xs, expect):
         _check(x, e, seed)
     device_clean()
+
+
+@pytest.mark.parametrize("seed", [0, 12])
+def test_codes_are_those_of_the_float32_restatement(seed):
+    # The header fixes every rounding of the moments, so the same steps in numpy's float32 give the
+    # same codes and scales, bit for bit.
+    f, n = np.float32, 100 * 256
+    x = _make(np.random.default_rng(21), n, "e4m3", torch.float32, torch.float32)
+    s = np.repeat(x.scale.cpu().numpy(), 256, axis=0)
+    g, m, r = (a.float().cpu().numpy() for a in (x.grad, x.m, x.v))
+    b1, b2 = f(C["beta1"]), f(C["beta2"])
+    m, r = m * s[:, 0], r * s[:, 1]
+    m = b1 * m + (f(1) - b1) * g
+    r = np.sqrt(b2 * (r * r) + ((f(1) - b2) * g) * g)
+    MultiAdamW([x]).step(_cfg(), t=3, seed=seed)
+    torch.cuda.synchronize()
+    h = O.element_bits(n, 0, seed) if seed else None
+    for k, (w, codes) in enumerate(((m, x.m), (r, x.v))):
+        top = np.abs(w).reshape(-1, 256).max(1)
+        y = np.abs(w * np.repeat(f(448) * (f(1) / top), 256))
+        assert y.dtype == f
+        grid = O.e4m3_grid(y.astype(np.float64))
+        rnd = None if h is None else (h & np.uint64(0xFFFF) if k == 0 else h >> np.uint64(16)).astype(np.float64)
+        q = (np.rint(y / grid) if rnd is None else np.floor(y / grid + rnd / 65536)) * grid
+        q = np.minimum(np.maximum(q, 2.0 ** -9 if k else 0), 448) * np.where(w < 0, -1, 1)
+        assert np.array_equal(codes.float().cpu().numpy(), q)
+        assert np.array_equal(x.scale[:, k].cpu().numpy(), top * (f(1) / f(448)))
 
 
 def test_more_tensors_than_one_launch_holds():
@@ -259,3 +292,9 @@ def test_reset_and_step_count():
         x = opt.tensors[0]
         assert opt.t == 0 and not x.m.view(torch.uint8).any() and not x.v.view(torch.uint8).any()
         assert x.scale is None or not x.scale.any()
+
+
+def test_square_root_of_every_float():
+    bad = torch.ones(1, dtype=torch.int64, device="cuda")
+    P.poetx_test_sqrt(0x0D800000, 0x7F7FFFFF, bad)
+    assert int(bad) == 0
