@@ -228,6 +228,54 @@ poetx_status poetx_xq_merge(const poetx_desc* desc, int8_t* W0q, float* W0s, con
                             const int32_t* perm_L_new, const int32_t* perm_R_new, float* theta_R,
                             float* theta_P, void* workspace, size_t ws_bytes, poetx_stream stream);
 
+/* ----------------------------------------------------------------------------------- MX4
+ * W0' (or any frozen weight) in 4 bits, in the OCP microscaling format MXFP4: e2m1 codes (sign, two
+ * exponent bits, one mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6) and one power-of-two scale for
+ * POETX_MX4_BLOCK = 32 consecutive columns of a row: 4.25 bits a weight, half of POET-XQ's.  The pages
+ * give no 4-bit form; this one is the published format with its conversion rule:
+ *   amax = max |W[r, 32 g .. 32 g + 31]|,  e = clamp(floor(log2 amax) - 2, -127, 127),
+ *   code = e2m1(W[r, c] / 2^e), to nearest, ties to the even code, saturating at 6;
+ *   an all-zero block has e = -127; a block with an infinity or a NaN is stored as NaN.
+ *   codes  uint8 [rows, cols / 2]: byte c / 2 holds column c in its low nibble, c + 1 in its high one.
+ *   scales uint8 [rows, cols / 32]: e + 127, or 255 for NaN (E8M0; float8_e8m0fnu of other libraries).
+ * cols is a multiple of 32 (UNSUPPORTED_SHAPE otherwise); W is row-major, float32 or bf16.  The
+ * conversion is exact up to the rounding to a code, so codes depend on W's values alone.
+ *
+ * poetx_mx4_quantize:   W dtype [rows, cols] (in) -> codes, scales (out).
+ * poetx_mx4_dequantize: codes, scales (in) -> W bf16 [rows, cols] (out): the exact value, but that magnitudes of
+ *                       2^128 and more (only scales of 2^126 and 2^127 have them) become infinities.
+ * rows == 0 or cols == 0 launches nothing. */
+#define POETX_MX4_BLOCK 32
+poetx_status poetx_mx4_quantize(poetx_dtype dtype, int rows, int cols, const void* W, uint8_t* codes,
+                                uint8_t* scales, poetx_stream stream);
+poetx_status poetx_mx4_dequantize(int rows, int cols, const uint8_t* codes, const uint8_t* scales, void* W,
+                                  poetx_stream stream);
+
+/* Product with an MX4 weight W [d_out, d_in]: a merged layer when serving (from one token on), or
+ * the frozen part of a training step.
+ *   adjoint = 0:  Y [n, d_out] = X [n, d_in] . W^T        adjoint = 1:  Y [n, d_in] = X [n, d_out] . W
+ * X and Y bf16, row-major, not overlapping; sums in float32, rounded once.  d_in a multiple of 32, d_out of 8
+ * (UNSUPPORTED_SHAPE otherwise).  n_tokens == 0 launches nothing.  The same arguments give the same bits. */
+poetx_status poetx_mx4_matmul(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
+                              const uint8_t* scales, void* Y, poetx_stream stream);
+
+/* The POET-X layer on an MX4 W0', as the poetx_xq_ calls on an int8 one: POETX_BF16 and POETX_MEM only
+ * (INVALID_ARG otherwise), every block size of poetx_desc, workspace poetx_workspace_size(desc, n_tokens).
+ *   codes uint8 [d_out, d_in / 2], scales uint8 [d_out, d_in / 32]: of W0' = Pi_L W0 Pi_R^T.
+ * poetx_mx4_merge quantises the new W0' (rounded to bf16 first) into codes, scales (in/out). */
+poetx_status poetx_mx4_forward(const poetx_desc* desc, int n_tokens, const void* X, const uint8_t* codes,
+                               const uint8_t* scales, const int32_t* perm_L, const int32_t* perm_R, const void* Q_R,
+                               const void* Q_P, void* Y, void* workspace, size_t ws_bytes, poetx_stream stream);
+poetx_status poetx_mx4_backward(const poetx_desc* desc, int n_tokens, const void* dY, const void* X,
+                                const uint8_t* codes, const uint8_t* scales, const int32_t* perm_L,
+                                const int32_t* perm_R, const void* Q_R, const void* Q_P, const float* theta_R,
+                                const float* theta_P, void* dX, float* grad_theta_R, float* grad_theta_P,
+                                void* workspace, size_t ws_bytes, poetx_stream stream);
+poetx_status poetx_mx4_merge(const poetx_desc* desc, uint8_t* codes, uint8_t* scales, const void* Q_R, const void* Q_P,
+                             const int32_t* perm_L_old, const int32_t* perm_R_old, const int32_t* perm_L_new,
+                             const int32_t* perm_R_new, float* theta_R, float* theta_P, void* workspace,
+                             size_t ws_bytes, poetx_stream stream);
+
 /* ------------------------------------------------------ weight-centric comparator (not the path)
  * The original POET order of evaluation, for comparison with the input-centric path above
  * (replication review, "Summary": POET-X's speed-ups are measured against forming the
@@ -376,7 +424,7 @@ typedef enum {
   POETX_KC_CNP_GEMM = 3,     /* CNP forward (the on-chip kernel, or its products for F32 / b = 512) */
   POETX_KC_MERGE_GEMM = 4,   /* BD_R W0' BD_P of the merge                                  */
   POETX_KC_PERMUTE = 5,      /* feature-dimension gather / scatter                          */
-  POETX_KC_ELEMENTWISE = 6,  /* unpack, pack, split-K reduction, permutation inverse        */
+  POETX_KC_ELEMENTWISE = 6,  /* unpack, pack, split-K reduction, permutation inverse, codes */
   POETX_KC_TEST_GEMM = 7,    /* poetx_test_gemm                                              */
   POETX_KC_OPTIMIZER = 8,    /* poetx_adamw_step                                             */
   POETX_KC_W_GEMM_ADJ = 9,   /* dV = dZ W0' (with the BD_P adjoint fused for b = 256)        */

@@ -23,12 +23,15 @@ __all__ = [
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
     "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
+    "poetx_mx4_quantize", "poetx_mx4_dequantize", "poetx_mx4_matmul", "poetx_mx4_forward", "poetx_mx4_backward",
+    "poetx_mx4_merge", "POETX_MX4_BLOCK",
 ]
 
 POETX_F32, POETX_BF16 = 0, 1
 POETX_FAST, POETX_MEM = 0, 1
 POETX_MOMENT_F32, POETX_MOMENT_E4M3 = 0, 1
 POETX_MOMENT_BLOCK = 256
+POETX_MX4_BLOCK = 32
 STATUS = {
     0: "POETX_OK", 1: "POETX_ERR_INVALID_ARG", 2: "POETX_ERR_UNSUPPORTED_SHAPE", 3: "POETX_ERR_ALIGNMENT",
     4: "POETX_ERR_WORKSPACE", 5: "POETX_ERR_CUDA", 6: "POETX_ERR_DEVICE_TIMEOUT",
@@ -101,6 +104,12 @@ _SIGNATURES = {
     "poetx_xq_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_xq_backward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_xq_merge": (_I, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "poetx_mx4_quantize": (_I, [_I, _I, _I, _P, _P, _P, _P]),
+    "poetx_mx4_dequantize": (_I, [_I, _I, _P, _P, _P, _P]),
+    "poetx_mx4_matmul": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "poetx_mx4_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "poetx_mx4_backward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
+    "poetx_mx4_merge": (_I, [_D, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_check_permutation": (_I, [_P, _I]),
     "poetx_fourperm_workspace_size": (_SZ, [_D, _I]),
     "poetx_fourperm_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
@@ -366,6 +375,74 @@ def poetx_xq_merge(desc, W0q, W0s, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new,
     _check(lib().poetx_xq_merge(ctypes.byref(desc), _ptr(W0q), _ptr(W0s), _ptr(Q_R), _ptr(Q_P), _ptr(perm_L_old),
                                 _ptr(perm_R_old), _ptr(perm_L_new), _ptr(perm_R_new), _ptr(theta_R),
                                 _ptr(theta_P), _ptr(workspace), ws_bytes, _stream(stream)), "poetx_xq_merge")
+
+
+def _check_mx4(rows, cols, codes, scales):
+    import torch
+    # Codes of two weights a byte and E8M0 scales, as uint8 or under torch's own names for them.
+    for x, name, numel, own in ((codes, "codes", rows * cols // 2, "float4_e2m1fn_x2"),
+                                (scales, "scales", rows * cols // POETX_MX4_BLOCK, "float8_e8m0fnu")):
+        _need(x, name, numel)
+        if hasattr(x, "dtype") and x.dtype not in (torch.uint8, getattr(torch, own, torch.uint8)):
+            raise ValueError(f"{name}: expected torch.uint8 or torch.{own}, got {x.dtype}")
+
+
+def poetx_mx4_quantize(dtype, rows, cols, W, codes, scales, stream=None):
+    import torch
+    _need(W, "W", rows * cols, torch.bfloat16 if dtype == POETX_BF16 else torch.float32)
+    _check_mx4(rows, cols, codes, scales)
+    _check(lib().poetx_mx4_quantize(dtype, rows, cols, _ptr(W), _ptr(codes), _ptr(scales), _stream(stream)),
+           "poetx_mx4_quantize")
+
+
+def poetx_mx4_dequantize(rows, cols, codes, scales, W, stream=None):
+    import torch
+    _need(W, "W", rows * cols, torch.bfloat16)
+    _check_mx4(rows, cols, codes, scales)
+    _check(lib().poetx_mx4_dequantize(rows, cols, _ptr(codes), _ptr(scales), _ptr(W), _stream(stream)),
+           "poetx_mx4_dequantize")
+
+
+def poetx_mx4_matmul(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, stream=None):
+    import torch
+    _need(X, "X", n_tokens * (d_out if adjoint else d_in), torch.bfloat16)
+    _need(Y, "Y", n_tokens * (d_in if adjoint else d_out), torch.bfloat16)
+    _check_mx4(d_out, d_in, codes, scales)
+    _check(lib().poetx_mx4_matmul(1 if adjoint else 0, n_tokens, d_in, d_out, _ptr(X), _ptr(codes), _ptr(scales),
+                                  _ptr(Y), _stream(stream)), "poetx_mx4_matmul")
+
+
+def poetx_mx4_forward(desc, n_tokens, X, codes, scales, perm_L, perm_R, Q_R, Q_P, Y, workspace, ws_bytes=None,
+                      stream=None):
+    _check_layer(desc, n_tokens, X=X, perm_L=perm_L, perm_R=perm_R, Q_R=Q_R, Q_P=Q_P, Y=Y)
+    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    _check(lib().poetx_mx4_forward(ctypes.byref(desc), n_tokens, _ptr(X), _ptr(codes), _ptr(scales), _ptr(perm_L),
+                                   _ptr(perm_R), _ptr(Q_R), _ptr(Q_P), _ptr(Y), _ptr(workspace), ws_bytes,
+                                   _stream(stream)), "poetx_mx4_forward")
+
+
+def poetx_mx4_backward(desc, n_tokens, dY, X, codes, scales, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P, dX,
+                       grad_theta_R, grad_theta_P, workspace, ws_bytes=None, stream=None):
+    _check_layer(desc, n_tokens, dY=dY, X=X, perm_L=perm_L, perm_R=perm_R, Q_R=Q_R, Q_P=Q_P, theta_R=theta_R,
+                 theta_P=theta_P, dX=dX, grad_theta_R=grad_theta_R, grad_theta_P=grad_theta_P)
+    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    _check(lib().poetx_mx4_backward(ctypes.byref(desc), n_tokens, _ptr(dY), _ptr(X), _ptr(codes), _ptr(scales),
+                                    _ptr(perm_L), _ptr(perm_R), _ptr(Q_R), _ptr(Q_P), _ptr(theta_R), _ptr(theta_P),
+                                    _ptr(dX), _ptr(grad_theta_R), _ptr(grad_theta_P), _ptr(workspace), ws_bytes,
+                                    _stream(stream)), "poetx_mx4_backward")
+
+
+def poetx_mx4_merge(desc, codes, scales, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new, perm_R_new, theta_R, theta_P,
+                    workspace, ws_bytes=None, stream=None):
+    _check_layer(desc, Q_R=Q_R, Q_P=Q_P, perm_L_old=perm_L_old, perm_R_old=perm_R_old, perm_L_new=perm_L_new,
+                 perm_R_new=perm_R_new, theta_R=theta_R, theta_P=theta_P)
+    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
+    _check(lib().poetx_mx4_merge(ctypes.byref(desc), _ptr(codes), _ptr(scales), _ptr(Q_R), _ptr(Q_P), _ptr(perm_L_old),
+                                 _ptr(perm_R_old), _ptr(perm_L_new), _ptr(perm_R_new), _ptr(theta_R), _ptr(theta_P),
+                                 _ptr(workspace), ws_bytes, _stream(stream)), "poetx_mx4_merge")
 
 
 def poetx_check_permutation(perm, n=None):

@@ -53,6 +53,7 @@ struct GemmDesc {
   bool a_mn = false, b_mn = false;
   Epilogue epi;
   const float* b_scale = nullptr;  // set: B is int8 codes, B row r scaled by b_scale[r] (W0' GEMM only)
+  const uint8_t* b_mx4 = nullptr;  // set: B is MX4 codes (two a byte), these their block scales (W0' GEMM only)
   // B was not written by the kernel launched just before this one (W0' GEMM only): its first
   // stages may be requested before the wait for that kernel.
   bool b_static = false;

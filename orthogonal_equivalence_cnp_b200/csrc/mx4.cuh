@@ -1,0 +1,375 @@
+// MX4: a weight in 4 bits (the OCP microscaled format MXFP4) and its products with bf16 activations.
+//
+// codes[r][c / 2] holds the e2m1 codes of columns c (low nibble) and c + 1; scales[r][c / 32] is the
+// exponent plus 127 of the power of two that 32 consecutive columns share (255: NaN).  A code is
+// sign, two exponent bits (bias 1), one mantissa bit: 0, 1/2, 1, 3/2, 2, 3, 4, 6.
+#pragma once
+
+#include <cuda_fp4.h>
+
+#include "common.cuh"
+#include "sm100.cuh"
+
+namespace poetx {
+
+constexpr int KID_MX4 = 9;  // kernel id in the device error word
+
+// ------------------------------------------------------------------- codes to bf16, exactly
+// bf16x2 factors of one scale: 2^(e - 1) as a product of two, since it may pass bf16's range (the
+// second is 1 for e <= 128, so only scales above 2 take two multiplications).
+struct Mx4Scale {
+  uint32_t f1, f2;
+  bool two;
+};
+__device__ __forceinline__ Mx4Scale mx4_scale(uint32_t e) {
+  Mx4Scale s;
+  const uint32_t lo = min(e, 128u);
+  s.f1 = e == 255u ? 0x7FC07FC0u : (lo + 126u) * 0x00800080u;
+  s.f2 = (e - 1u) * 0x00800080u;  // 2^(e - 128), read only for 128 < e < 255
+  s.two = e > 128u && e < 255u;
+  return s;
+}
+__device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+// Eight codes (w: code e in bits 4e..4e+3) to eight bf16 values in column order.  The code's three
+// magnitude bits, moved to the lowest exponent bits and the highest mantissa bit of a bf16, are the value times
+// 2^-126 (a subnormal for 0 and 1/2), so one exact product with 2^126 times the scale finishes it.  Per pair:
+// one byte permutation puts both codes at the tops of their halves, one shift and two masks place the bits.
+__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, const Mx4Scale& s) {
+  const uint32_t w4 = w << 4;
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint32_t t = __byte_perm(w4, w, ((4 + j) << 12) | ((4 + j) << 8) | (j << 4) | j);
+    o[j] = bf16x2_mul((t & 0x80008000u) | ((t >> 6) & 0x01C001C0u), s.f1);
+  }
+  if (s.two) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = bf16x2_mul(o[j], s.f2);
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// --------------------------------------------------------------------------- quantisation
+// A thread takes eight columns, four threads one scale: the block's largest magnitude meets by two
+// shuffles, its exponent gives the scale, and the values times the scale's inverse (a power of two: exact)
+// round to nearest even in the conversion instruction.  One pass, coalesced both ways: HBM bound.
+template <bool BF>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restrict__ W, long chunks,
+                                                           uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
+  sm100::griddep_wait();
+  const long stride = (long)gridDim.x * blockDim.x;
+  // chunks is a multiple of 4, and so is every thread's group: the shuffles' partners are all here or none is.
+  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < chunks; i += stride) {
+    const uint32_t mask = __activemask();
+    float x[8];
+    if (BF) {
+      const uint4 u = reinterpret_cast<const uint4*>(W)[i];
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    } else {
+      const float4 a = reinterpret_cast<const float4*>(W)[2 * i], b = reinterpret_cast<const float4*>(W)[2 * i + 1];
+      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
+      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    }
+    uint32_t top = 0u;  // magnitudes ordered as integers: infinities and NaN end on top
+#pragma unroll
+    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(x[e])));
+    top = max(top, __shfl_xor_sync(mask, top, 1));
+    top = max(top, __shfl_xor_sync(mask, top, 2));
+    uint32_t w = 0u, scale = 255u;  // a block with a NaN or an infinity reads back as NaN
+    if (top < 0x7F800000u) {
+      scale = (uint32_t)max((int)(top >> 23) - 2, 0);
+      // 2^(127 - scale); scale <= 252, and 2^-126 is the smallest normal number.
+      const float inv = scale <= 253u ? __uint_as_float((254u - scale) << 23) : 0.f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_E2M1,
+                                                cudaRoundNearest)
+             << (8 * e);
+    }
+    codes[i] = w;
+    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)scale;
+  }
+}
+
+// bf16 values of codes and scales, eight columns per thread step.
+__global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
+                                                             const uint8_t* __restrict__ scales, long chunks,
+                                                             uint4* __restrict__ W) {
+  sm100::griddep_wait();
+  const long stride = (long)gridDim.x * blockDim.x;
+  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < chunks; i += stride)
+    W[i] = mx4_decode8(codes[i], mx4_scale(scales[i >> 2]));
+}
+
+// -------------------------------------------------------------------------------- product
+// Y[t][m] = sum_k w(m, k) X[t][k] with w(m, k) = W[m][k] (forward: m an output, k an input feature) or W[k][m]
+// (adjoint), X and Y bf16, sums in fp32.
+//
+// The weight is the 128-row operand (MH of them per CTA: 128 or 256 features), the tokens are the columns (TN of
+// them, a multiple of 16 up to 256), so that few tokens waste nothing of the tile.  One warp streams X tiles and
+// code tiles with TMA into a ring; eight converter warps turn a code tile into a bf16 tile in the
+// 128-byte-swizzled layout of the tensor core (forward: K-major, adjoint: MN-major) in a ring of its own; one
+// thread issues tcgen05.mma; the accumulators (features in TMEM lanes, tokens in columns) go through shared
+// memory as fp32.  Where the tiles alone do not fill the SMs, a cluster of up to 8 CTAs splits K and each CTA
+// sums its share of the tokens over the cluster's shared memory, in a fixed order.
+struct Mx4Args {
+  int M, N, K;           // features out, tokens, features in
+  int TN;                // tokens per tile
+  int xs, ws;            // ring depths: X and codes, converted weight
+  int splits;            // CTAs of a cluster, along K
+  const uint8_t* scales;
+  long pitch;            // scales per row of the weight
+  __nv_bfloat16* Y;
+};
+
+constexpr int MX4_CONV = 256;                    // converter threads (warps 0..7)
+constexpr int MX4_THREADS = MX4_CONV + 64;       // + one producer warp, one MMA warp
+constexpr int MX4_BK = 64;
+constexpr int MX4_MAX_RING = 16;
+__host__ __device__ constexpr uint32_t mx4_w_bytes(int mh) { return (uint32_t)mh * 128 * MX4_BK * 2; }
+__host__ __device__ constexpr uint32_t mx4_code_bytes(int mh) { return (uint32_t)mh * 128 * MX4_BK / 2; }
+__host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int xs, int ws) {
+  return (size_t)xs * (tn * MX4_BK * 2 + mx4_code_bytes(mh)) + (size_t)ws * mx4_w_bytes(mh) + 1024 + 512;
+}
+
+template <int MH, bool ADJ>
+__global__ void __launch_bounds__(MX4_THREADS, 1)
+    mx4_gemm_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC, const Mx4Args a) {
+  using namespace sm100;
+  constexpr uint32_t W_BYTES = mx4_w_bytes(MH), C_BYTES = mx4_code_bytes(MH);
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t x_bytes = (uint32_t)a.TN * MX4_BK * 2;
+  uint8_t* wring = smem + (size_t)a.xs * x_bytes;
+  uint8_t* cring = wring + (size_t)a.ws * W_BYTES;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(cring + (size_t)a.xs * C_BYTES);
+  const uint32_t sx = smem_u32(smem), sw = smem_u32(wring), sc = smem_u32(cring), sb = smem_u32(bars);
+  auto full = [&](int s) { return sb + 8u * s; };                            // X and codes have arrived
+  auto empty = [&](int s) { return sb + 8u * (MX4_MAX_RING + s); };          // the products of the stage are done
+  auto conv = [&](int s) { return sb + 8u * (2 * MX4_MAX_RING + s); };       // weight tile converted
+  auto wfree = [&](int s) { return sb + 8u * (2 * MX4_MAX_RING + 4 + s); };  // weight tile consumed
+  const uint32_t accum = sb + 8u * (2 * MX4_MAX_RING + 8);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * MX4_MAX_RING + 9);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * (MH * 128);
+  const int n0 = blockIdx.y * a.TN;
+  const int KT = (a.K + MX4_BK - 1) / MX4_BK;
+  const int kt0 = (int)((long)KT * split / a.splits), nkt = (int)((long)KT * (split + 1) / a.splits) - kt0;
+  // TMEM columns: MH accumulators of TN, a power of two from 32 up.
+  uint32_t cols = 32;
+  while (cols < (uint32_t)(MH * a.TN)) cols <<= 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < a.xs; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int s = 0; s < a.ws; ++s) {
+      mbar_init(conv(s), MX4_CONV / 32);
+      mbar_init(wfree(s), 1);
+    }
+    mbar_init(accum, 1);
+    fence_mbar_init();
+    fence_proxy_async_smem();
+    prefetch_tmap(&tmX);
+    prefetch_tmap(&tmC);
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(holder), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *holder;
+  griddep_wait();  // X, and just after a quantisation the codes, come from earlier launches
+
+  if (warp == 8) {
+    if (lane == 0) {
+      // ---------------- TMA producer
+      for (int i = 0; i < nkt; ++i) {
+        const int s = i % a.xs;
+        if (!mbar_wait(empty(s), ((uint32_t)(i / a.xs) & 1u) ^ 1u, KID_MX4, 1)) break;
+        mbar_arrive_expect_tx(full(s), x_bytes + C_BYTES);
+        const int k0 = (kt0 + i) * MX4_BK;
+        if (!ADJ) {
+          tma_load_2d(sc + s * C_BYTES, &tmC, full(s), k0 / 2, m0);  // 32 bytes x 128 MH rows
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2 * MH; ++h)  // 32 bytes (64 features) x 64 rows each
+            tma_load_2d(sc + s * C_BYTES + h * 2048, &tmC, full(s), m0 / 2 + 32 * h, k0);
+        }
+        tma_load_2d(sx + s * x_bytes, &tmX, full(s), k0, n0);
+      }
+    }
+  } else if (warp == 9) {
+    if (lane == 0) {
+      // ---------------- MMA issuer
+      const uint32_t idesc = idesc_bf16_f32(128, a.TN, ADJ, false);
+      for (int i = 0; i < nkt; ++i) {
+        const int s = i % a.xs, t = i % a.ws;
+        if (!mbar_wait(full(s), (uint32_t)(i / a.xs) & 1u, KID_MX4, 2)) break;
+        if (!mbar_wait(conv(t), (uint32_t)(i / a.ws) & 1u, KID_MX4, 3)) break;
+        tc_fence_after();
+        const uint32_t xa = sx + s * x_bytes, wa = sw + t * W_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < MX4_BK / 16; ++kk) {
+          const uint64_t bd = smem_desc_sw128(xa + kk * 32, 16, 1024);
+#pragma unroll
+          for (int h = 0; h < MH; ++h) {
+            const uint64_t ad = ADJ ? smem_desc_sw128(wa + h * 16384 + kk * 2048, 8192, 1024)
+                                    : smem_desc_sw128(wa + h * 16384 + kk * 32, 16, 1024);
+            mma_bf16(tmem + (uint32_t)(h * a.TN), ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+          }
+        }
+        mma_commit(empty(s));
+        mma_commit(wfree(t));
+      }
+      mma_commit(accum);
+    }
+  } else {
+    // ---------------- converters: MH blocks of 32 codes per thread and k step
+    const int ct = threadIdx.x;
+    const uint8_t* scale_at[MH];
+    long scale_step;
+    bool live[MH];
+    int src[MH], dst[MH], key;
+    if (!ADJ) {
+      const int row = MH == 1 ? (ct & 127) : ct;
+      key = row & 7;
+      scale_step = MX4_BK / 32;
+#pragma unroll
+      for (int u = 0; u < MH; ++u) {
+        const int b = MH == 1 ? ct >> 7 : u;  // which 32 of the 64 columns
+        src[u] = row * 32 + b * 16;
+        dst[u] = row * 128 + 0 * b;
+        live[u] = m0 + row < a.M;
+        scale_at[u] = a.scales + (long)(m0 + row) * a.pitch + (long)kt0 * scale_step + b;
+      }
+    } else {
+      const int k = ct & 63;
+      key = k & 7;
+      scale_step = MX4_BK * a.pitch;
+#pragma unroll
+      for (int u = 0; u < MH; ++u) {
+        const int b = MH == 1 ? ct >> 6 : (ct >> 6) * 2 + u;  // which 32 of the 128 MH features
+        src[u] = (b >> 1) * 2048 + k * 32 + (b & 1) * 16;
+        dst[u] = (b >> 1) * 8192 + k * 128;
+        live[u] = m0 + 32 * b < a.M;
+        scale_at[u] = a.scales + ((long)kt0 * MX4_BK + k) * a.pitch + m0 / 32 + b;
+      }
+    }
+    // The scale of step i; past the weight's edge, where the codes are zeros, any finite one does.
+    auto load_scale = [&](int i, int u) -> uint32_t {
+      const bool ok = ADJ ? live[u] && (kt0 + i) * MX4_BK + (ct & 63) < a.K
+                          : live[u] && (kt0 + i) * MX4_BK + 32 * (MH == 1 ? ct >> 7 : u) < a.K;
+      return i < nkt && ok ? (uint32_t)__ldg(scale_at[u] + (long)i * scale_step) : 127u;
+    };
+    // Scales are fetched four steps ahead, four steps at a time.
+    uint32_t cur[4][MH], nxt[4][MH];
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int u = 0; u < MH; ++u) nxt[q][u] = load_scale(q, u);
+    bool ok = true;
+    for (int i0 = 0; i0 < nkt && ok; i0 += 4) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int u = 0; u < MH; ++u) {
+          cur[q][u] = nxt[q][u];
+          nxt[q][u] = load_scale(i0 + 4 + q, u);
+        }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q;
+        if (i < nkt && ok) {
+          const int s = i % a.xs, t = i % a.ws;
+          ok = mbar_wait(full(s), (uint32_t)(i / a.xs) & 1u, KID_MX4, 4);
+          ok = ok && mbar_wait(wfree(t), ((uint32_t)(i / a.ws) & 1u) ^ 1u, KID_MX4, 5);
+          ok = __all_sync(0xffffffffu, ok);
+          if (ok) {
+            const uint8_t* codes = cring + s * C_BYTES;
+            uint8_t* tile = wring + t * W_BYTES;
+#pragma unroll
+            for (int u = 0; u < MH; ++u) {
+              const uint4 c = *reinterpret_cast<const uint4*>(codes + src[u]);
+              const Mx4Scale f = mx4_scale(cur[q][u]);
+              const int half = ADJ ? (MH == 1 ? (ct >> 6) & 1 : u) : (MH == 1 ? ct >> 7 : u);  // 64-byte half of the row
+              const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                *reinterpret_cast<uint4*>(tile + dst[u] + (((4 * half + j) ^ key) << 4)) = mx4_decode8(w[j], f);
+            }
+            fence_proxy_async_smem();  // the tensor core reads what the threads wrote
+            __syncwarp();
+            if (lane == 0) mbar_arrive(conv(t));
+          }
+        }
+      }
+    }
+  }
+  __syncwarp();
+
+  // ---------------- epilogue, one 128-feature half after the other: fp32 sums through shared memory
+  bool ok = mbar_wait(accum, 0, KID_MX4, 6);
+  ok = __all_sync(0xffffffffu, ok);
+  tc_fence_after();
+  griddep_launch();
+  float* red = reinterpret_cast<float*>(smem);  // [TN][128]: the rings are idle (every load has been consumed)
+  const int share = a.TN / a.splits, c_lo = split * share;
+#pragma unroll 1
+  for (int h = 0; h < MH; ++h) {
+    if (warp < 8 && ok) {
+      // Warp w: lanes 32 (w % 4).., token columns of the half w / 4.
+      const int m = (warp & 3) * 32 + lane, half_n = a.TN / 2;
+      const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN + (warp >> 2) * half_n);
+      float* out = red + (size_t)(warp >> 2) * half_n * 128 + m;
+      for (int c = 0; c < half_n; c += 8) {
+        uint32_t v[8];
+        tmem_ld_32x32b_x8(t0 + (uint32_t)c, v);
+        tmem_wait_ld();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[(size_t)(c + j) * 128] = __uint_as_float(v[j]);
+      }
+    }
+    if (a.splits > 1) cluster_sync_all(); else __syncthreads();
+    if (ok) {
+      // Eight features of one token per step: sum over the cluster, round once, 16-byte store.
+      for (int e = threadIdx.x; e < share * 16; e += MX4_THREADS) {
+        const int c = c_lo + (e >> 4), f = (e & 15) * 8;
+        const int n = n0 + c, m = m0 + h * 128 + f;
+        if (n < a.N && m < a.M) {
+          float x[8] = {};
+          const uint32_t at = smem_u32(red + (size_t)c * 128 + f);
+          for (int r = 0; r < a.splits; ++r) {
+            float y[8];
+            ld_cluster_v4(a.splits > 1 ? mapa_shared(at, (uint32_t)r) : at, y);
+            ld_cluster_v4((a.splits > 1 ? mapa_shared(at, (uint32_t)r) : at) + 16, y + 4);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] += y[j];
+          }
+          *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
+              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+        }
+      }
+    }
+    // The peers have read this CTA's sums before it reuses them or exits.
+    if (a.splits > 1) cluster_sync_all(); else __syncthreads();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, cols);
+}
+
+}  // namespace poetx

@@ -17,6 +17,7 @@
 #include "common.cuh"
 #include "elementwise.cuh"
 #include "gemm.cuh"
+#include "mx4.cuh"
 #include "optim.cuh"
 #include "sm100.cuh"
 #include "cnp_onchip.cuh"
@@ -398,7 +399,8 @@ poetx_status reduce_splits(const float* part, int splits, long rows, int cols, f
 // W0' GEMM fused with the following block-diagonal factor (b = 256 only): out2 = D . Q^T
 // (q_mn = false, forward BD_R) or D . Q (q_mn = true, adjoint of BD_P), D also stored to d1.
 bool bd_fusable(int dt, int b, const GemmDesc& g) {
-  return dt == BF16 && b == 256 && !g.a_mn && g.N % 256 == 0 && g.batch == 1 && g.splits == 1 && g.K > 0;
+  return dt == BF16 && b == 256 && !g.a_mn && g.N % 256 == 0 && g.batch == 1 && g.splits == 1 && g.K > 0 &&
+         g.b_mx4 == nullptr;
 }
 
 template <bool BMN, bool QMN>
@@ -516,9 +518,93 @@ poetx_status run_w_gemm_q8(const GemmDesc& g, const void* Q, long q_rows, bool q
   return launch_w256<true, true, true>(g, Q, q_rows, out2, ld2, st, cls);
 }
 
+// ------------------------------------------------------------------------------ MX4 products
+struct Mx4Plan {
+  int mh, tn, xs, ws, splits;
+};
+Mx4Plan mx4_plan(long M, long N, long K) {
+  Mx4Plan p;
+  const long nt = (N + 255) / 256;
+  p.tn = (int)(((N + nt - 1) / nt + 15) / 16 * 16);
+  // Two halves of 128 features per CTA (the X tile is read once for both) while that still
+  // occupies three quarters of the SMs.
+  const long t2 = (M + 255) / 256 * nt, kt = (K + MX4_BK - 1) / MX4_BK;
+  p.mh = 4 * t2 >= 3L * kNumSms ? 2 : 1;
+  const long tiles = p.mh == 2 ? t2 : (M + 127) / 128 * nt;
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 <= kNumSms && kt >= 8L * p.splits) p.splits *= 2;
+  p.ws = p.mh == 2 ? 2 : 3;
+  p.xs = MX4_MAX_RING;
+  while (p.xs > 4 && mx4_smem_bytes(p.mh, p.tn, p.xs, p.ws) > 227 * 1024) --p.xs;
+  return p;
+}
+
+template <int MH, bool ADJ>
+poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes, const uint8_t* scales, void* Y, int M,
+                        int N, int K, cudaStream_t st, int cls) {
+  static bool attr_done[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
+  auto kern = mx4_gemm_tc<MH, ADJ>;
+  if (!attr_done[dev]) {
+    if (!set_smem(kern, 227 * 1024)) return POETX_ERR_CUDA;
+    attr_done[dev] = true;
+  }
+  CUtensorMap tx, tc;
+  if (!make_tmap(&tx, X, 64, (uint32_t)p.tn)) return POETX_ERR_CUDA;
+  if (!make_tmap(&tc, codes, 32, ADJ ? 64 : MH * 128, U8)) return POETX_ERR_CUDA;
+  Mx4Args a;
+  a.M = M; a.N = N; a.K = K;
+  a.TN = p.tn; a.xs = p.xs; a.ws = p.ws; a.splits = p.splits;
+  a.scales = scales;
+  a.pitch = codes.cols / 16;
+  a.Y = static_cast<__nv_bfloat16*>(Y);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((M + MH * 128 - 1) / (MH * 128) * p.splits), (unsigned)((N + p.tn - 1) / p.tn), 1);
+  cfg.blockDim = dim3(MX4_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = mx4_smem_bytes(MH, p.tn, p.xs, p.ws);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)p.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = p.splits > 1 ? 2 : 1;
+  LaunchScope ls(cls, st);
+  if (cudaLaunchKernelEx(&cfg, kern, tx, tc, a) != cudaSuccess) return POETX_ERR_CUDA;
+  return last_launch();
+}
+
+// Y [n, M] = X [n, K] . W^T (forward: M = d_out, K = d_in) or X . W (adjoint: M = d_in, K = d_out)
+// with W [d_out, d_in] in MX4.  Checked by the callers: aligned pointers, d_in a multiple of 32,
+// d_out of 8.
+poetx_status mx4_product(bool adjoint, int n, int d_in, int d_out, const void* X, const uint8_t* codes,
+                         const uint8_t* scales, void* Y, cudaStream_t st, int cls) {
+  const int M = adjoint ? d_in : d_out, K = adjoint ? d_out : d_in;
+  const Mx4Plan p = mx4_plan(M, n, K);
+  if ((n + (long)p.tn - 1) / p.tn > 65535) return POETX_ERR_UNSUPPORTED_SHAPE;
+  const Operand x = view(X, n, K, K), c = view(codes, d_out, d_in / 2, d_in / 2);
+  if (adjoint)
+    return p.mh == 2 ? launch_mx4<2, true>(p, x, c, scales, Y, M, n, K, st, cls)
+                     : launch_mx4<1, true>(p, x, c, scales, Y, M, n, K, st, cls);
+  return p.mh == 2 ? launch_mx4<2, false>(p, x, c, scales, Y, M, n, K, st, cls)
+                   : launch_mx4<1, false>(p, x, c, scales, Y, M, n, K, st, cls);
+}
+
+// The W0' GEMM on an MX4 weight: plain bf16 store, no fused block factor.
+poetx_status run_w_gemm_mx4(const GemmDesc& g, cudaStream_t st, int cls) {
+  const int d_in = g.b_mn ? g.N : g.K, d_out = g.b_mn ? g.K : g.N;
+  return mx4_product(g.b_mn, g.M, d_in, d_out, g.A.base, static_cast<const uint8_t*>(g.B.base), g.b_mx4, g.epi.d1, st,
+                     cls);
+}
+
 // The W0' GEMM D = A . B^T -> d1, and (out2 != null, b = 256) out2 = D . Q^T or D . Q.
 poetx_status run_w_gemm(int dt, const GemmDesc& g, const void* Q, long q_rows, bool q_mn, void* out2, long ld2,
                         cudaStream_t st, int cls = POETX_KC_W_GEMM) {
+  if (g.b_mx4 != nullptr) return out2 == nullptr ? run_w_gemm_mx4(g, st, cls) : POETX_ERR_INVALID_ARG;
   if (g.b_scale != nullptr) return dt == BF16 ? run_w_gemm_q8(g, Q, q_rows, q_mn, out2, ld2, st, cls) : POETX_ERR_INVALID_ARG;
   if (out2 == nullptr) {
     if (!w256_ok(dt, g)) return run_gemm(dt, g, st, cls);
@@ -1048,8 +1134,15 @@ poetx_status check_ws(const void* ws, size_t have, size_t need) {
   return POETX_OK;
 }
 
+// How W0' is held: bf16 / fp32 values (neither set), int8 codes with per-row scales (POET-XQ), or
+// MX4 codes with their block scales.
+struct W0Codes {
+  const float* rows = nullptr;
+  const uint8_t* mx4 = nullptr;
+};
+
 // Forward chain into caller buffers; `Z` receives the W0'-GEMM output.
-poetx_status forward_chain(const poetx_desc* d, long n, const void* X, const void* W0p, const float* W0s,
+poetx_status forward_chain(const poetx_desc* d, long n, const void* X, const void* W0p, W0Codes W0s,
                            const int32_t* pL, const int32_t* pR, const void* QR, const void* QP, void* Y, void* Z,
                            char* U, char* V, char* Yp, cudaStream_t st, bool gathered = false) {
   const int dt = d->dtype, b = d->b;
@@ -1059,7 +1152,8 @@ poetx_status forward_chain(const poetx_desc* d, long n, const void* X, const voi
   g.M = (int)n; g.N = d->d_out; g.K = d->d_in;
   g.A = view(V, n, d->d_in, d->d_in);
   g.B = view(W0p, d->d_out, d->d_in, d->d_in);
-  g.b_scale = W0s;  // POET-XQ: W0' is int8 codes with per-row scales
+  g.b_scale = W0s.rows;
+  g.b_mx4 = W0s.mx4;
   g.b_static = true;  // W0' is the caller's, not the output of the launch before (BD_P)
   g.epi.d1 = Z; g.epi.d1_dtype = dt; g.epi.ld1 = d->d_out;
   if (Y == nullptr) return run_w_gemm(dt, g, nullptr, 0, false, nullptr, 0, st);  // recompute only (mem-mode backward)
@@ -1302,7 +1396,7 @@ poetx_status poetx_absorb(const poetx_desc* desc, const void* W0, const int32_t*
 }
 
 static poetx_status forward_impl(const poetx_desc* desc, int n_tokens, const void* X, const void* W0p,
-                                 const float* W0s, const int32_t* perm_L, const int32_t* perm_R, const void* Q_R,
+                                 W0Codes W0s, const int32_t* perm_L, const int32_t* perm_R, const void* Q_R,
                                  const void* Q_P, void* Y, void* saved, void* workspace, size_t ws_bytes,
                                  poetx_stream stream) {
   POETX_TRY(check_desc(desc));
@@ -1326,7 +1420,7 @@ static poetx_status forward_impl(const poetx_desc* desc, int n_tokens, const voi
 poetx_status poetx_forward(const poetx_desc* desc, int n_tokens, const void* X, const void* W0p,
                            const int32_t* perm_L, const int32_t* perm_R, const void* Q_R, const void* Q_P, void* Y,
                            void* saved, void* workspace, size_t ws_bytes, poetx_stream stream) {
-  return forward_impl(desc, n_tokens, X, W0p, nullptr, perm_L, perm_R, Q_R, Q_P, Y, saved, workspace, ws_bytes,
+  return forward_impl(desc, n_tokens, X, W0p, {}, perm_L, perm_R, Q_R, Q_P, Y, saved, workspace, ws_bytes,
                       stream);
 }
 
@@ -1389,7 +1483,7 @@ poetx_status poetx_cnp_forward(const poetx_desc* desc, int n_tokens, const void*
   if (n_tokens <= 0 || !cnp_fused_ok(b, dt)) {
     if (n_tokens < 0) return POETX_ERR_INVALID_ARG;
     POETX_TRY(poetx_cnp(desc, theta_R, theta_P, Q_R, Q_P, workspace, ws_bytes, stream));
-    return forward_impl(desc, n_tokens, X, W0p, nullptr, perm_L, perm_R, Q_R, Q_P, Y, saved, workspace, ws_bytes,
+    return forward_impl(desc, n_tokens, X, W0p, {}, perm_L, perm_R, Q_R, Q_P, Y, saved, workspace, ws_bytes,
                         stream);
   }
   if (desc->mode == POETX_FAST && saved == nullptr) return POETX_ERR_INVALID_ARG;
@@ -1414,12 +1508,12 @@ poetx_status poetx_cnp_forward(const poetx_desc* desc, int n_tokens, const void*
     POETX_TRY(cnp_fwd_fused(b, desc->k, sides, 2, stream));
     POETX_TRY(permute_cols(dt, X, desc->d_in, U, desc->d_in, n_tokens, desc->d_in, perm_R, nullptr, false, stream));
   }
-  return forward_chain(desc, n_tokens, X, W0p, nullptr, perm_L, perm_R, Q_R, Q_P, Y, Z, U, ws + f.V, ws + f.Yp,
+  return forward_chain(desc, n_tokens, X, W0p, {}, perm_L, perm_R, Q_R, Q_P, Y, Z, U, ws + f.V, ws + f.Yp,
                        stream, true);
 }
 
 static poetx_status backward_impl(const poetx_desc* desc, int n_tokens, const void* dY, const void* X,
-                                  const void* W0p, const float* W0s, const int32_t* perm_L, const int32_t* perm_R,
+                                  const void* W0p, W0Codes W0s, const int32_t* perm_L, const int32_t* perm_R,
                                   const void* Q_R, const void* Q_P, const float* theta_R, const float* theta_P,
                                   const void* saved, void* dX, float* grad_theta_R,
                                   float* grad_theta_P, void* workspace, size_t ws_bytes, poetx_stream stream) {
@@ -1475,7 +1569,8 @@ static poetx_status backward_impl(const poetx_desc* desc, int n_tokens, const vo
   g.M = (int)n; g.N = din; g.K = dout;
   g.A = view(ws + w.dZ, n, dout, dout);
   g.B = view(W0p, dout, din, din); g.b_mn = true;
-  g.b_scale = W0s;
+  g.b_scale = W0s.rows;
+  g.b_mx4 = W0s.mx4;
   g.b_static = true;  // W0' is the caller's, not the output of the launch before (dZ)
   g.epi.d1 = ws + w.dV; g.epi.d1_dtype = dt; g.epi.ld1 = din;
   const bool fused_du = bd_fusable(dt, b, g);
@@ -1514,7 +1609,7 @@ poetx_status poetx_backward(const poetx_desc* desc, int n_tokens, const void* dY
                             const float* theta_R, const float* theta_P, const void* saved,
                             void* dX, float* grad_theta_R, float* grad_theta_P, void* workspace, size_t ws_bytes,
                             poetx_stream stream) {
-  return backward_impl(desc, n_tokens, dY, X, W0p, nullptr, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P, saved,
+  return backward_impl(desc, n_tokens, dY, X, W0p, {}, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P, saved,
                        dX, grad_theta_R, grad_theta_P, workspace, ws_bytes, stream);
 }
 
@@ -1877,7 +1972,7 @@ poetx_status poetx_xq_forward(const poetx_desc* desc, int n_tokens, const void* 
                               const void* Q_P, void* Y, void* workspace, size_t ws_bytes, poetx_stream stream) {
   POETX_TRY(check_xq(desc));
   POETX_TRY(check_ptrs({W0q, W0s}));
-  return forward_impl(desc, n_tokens, X, W0q, W0s, perm_L, perm_R, Q_R, Q_P, Y, nullptr, workspace, ws_bytes,
+  return forward_impl(desc, n_tokens, X, W0q, {W0s, nullptr}, perm_L, perm_R, Q_R, Q_P, Y, nullptr, workspace, ws_bytes,
                       stream);
 }
 
@@ -1888,7 +1983,7 @@ poetx_status poetx_xq_backward(const poetx_desc* desc, int n_tokens, const void*
                                poetx_stream stream) {
   POETX_TRY(check_xq(desc));
   POETX_TRY(check_ptrs({W0q, W0s}));
-  return backward_impl(desc, n_tokens, dY, X, W0q, W0s, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P, nullptr,
+  return backward_impl(desc, n_tokens, dY, X, W0q, {W0s, nullptr}, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P, nullptr,
                        dX, grad_theta_R, grad_theta_P, workspace, ws_bytes, stream);
 }
 
@@ -1907,6 +2002,106 @@ poetx_status poetx_xq_merge(const poetx_desc* desc, int8_t* W0q, float* W0s, con
   POETX_TRY(merge_impl(desc, ws + m.M2, ws + m.T, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new, perm_R_new, theta_R,
                        theta_P, ws, stream));
   return xq_quantize(desc, ws + m.T, W0q, W0s, stream);
+}
+
+// ------------------------------------------------------------------------------------- MX4
+static poetx_status check_mx4(int d_in, int d_out) {
+  if (d_in <= 0 || d_out <= 0) return POETX_ERR_INVALID_ARG;
+  if (d_in % 32 || d_out % 8) return POETX_ERR_UNSUPPORTED_SHAPE;
+  return POETX_OK;
+}
+// The layer on an MX4 weight: as POET-XQ, bf16 and POET-Xmem; any block size (d is a multiple of 64).
+static poetx_status check_mx4_layer(const poetx_desc* desc) {
+  POETX_TRY(check_desc(desc));
+  if (desc->dtype != POETX_BF16 || desc->mode != POETX_MEM) return POETX_ERR_INVALID_ARG;
+  return check_mx4(desc->d_in, desc->d_out);
+}
+
+static poetx_status mx4_quantize(poetx_dtype dtype, long rows, long cols, const void* W, uint8_t* codes,
+                                 uint8_t* scales, cudaStream_t st) {
+  const long chunks = rows * cols / 8;
+  LaunchScope ls(POETX_KC_ELEMENTWISE, st);
+  if (launch_pdl(dtype == POETX_BF16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>, dim3(ew_grid(chunks)),
+                 dim3(256), 0, st, W, chunks, reinterpret_cast<uint32_t*>(codes), scales) != cudaSuccess)
+    return POETX_ERR_CUDA;
+  return last_launch();
+}
+
+static poetx_status mx4_dequantize(long rows, long cols, const uint8_t* codes, const uint8_t* scales, void* W,
+                                   cudaStream_t st) {
+  const long chunks = rows * cols / 8;
+  LaunchScope ls(POETX_KC_ELEMENTWISE, st);
+  if (launch_pdl(mx4_dequantize_kernel, dim3(ew_grid(chunks)), dim3(256), 0, st,
+                 reinterpret_cast<const uint32_t*>(codes), scales, chunks, static_cast<uint4*>(W)) != cudaSuccess)
+    return POETX_ERR_CUDA;
+  return last_launch();
+}
+
+poetx_status poetx_mx4_quantize(poetx_dtype dtype, int rows, int cols, const void* W, uint8_t* codes, uint8_t* scales,
+                                poetx_stream stream) {
+  if ((dtype != POETX_F32 && dtype != POETX_BF16) || rows < 0 || cols < 0) return POETX_ERR_INVALID_ARG;
+  if (cols % 32) return POETX_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || cols == 0) return POETX_OK;
+  POETX_TRY(check_ptrs({W, codes, scales}));
+  return mx4_quantize(dtype, rows, cols, W, codes, scales, stream);
+}
+
+poetx_status poetx_mx4_dequantize(int rows, int cols, const uint8_t* codes, const uint8_t* scales, void* W,
+                                  poetx_stream stream) {
+  if (rows < 0 || cols < 0) return POETX_ERR_INVALID_ARG;
+  if (cols % 32) return POETX_ERR_UNSUPPORTED_SHAPE;
+  if (rows == 0 || cols == 0) return POETX_OK;
+  POETX_TRY(check_ptrs({codes, scales, W}));
+  return mx4_dequantize(rows, cols, codes, scales, W, stream);
+}
+
+poetx_status poetx_mx4_matmul(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
+                              const uint8_t* scales, void* Y, poetx_stream stream) {
+  if ((adjoint != 0 && adjoint != 1) || n_tokens < 0) return POETX_ERR_INVALID_ARG;
+  POETX_TRY(check_mx4(d_in, d_out));
+  if (n_tokens == 0) return POETX_OK;
+  POETX_TRY(check_ptrs({X, codes, scales, Y}));
+  if (X == Y) return POETX_ERR_INVALID_ARG;
+  return mx4_product(adjoint != 0, n_tokens, d_in, d_out, X, codes, scales, Y, stream,
+                     adjoint ? POETX_KC_W_GEMM_ADJ : POETX_KC_W_GEMM);
+}
+
+poetx_status poetx_mx4_forward(const poetx_desc* desc, int n_tokens, const void* X, const uint8_t* codes,
+                               const uint8_t* scales, const int32_t* perm_L, const int32_t* perm_R, const void* Q_R,
+                               const void* Q_P, void* Y, void* workspace, size_t ws_bytes, poetx_stream stream) {
+  POETX_TRY(check_mx4_layer(desc));
+  POETX_TRY(check_ptrs({codes, scales}));
+  return forward_impl(desc, n_tokens, X, codes, {nullptr, scales}, perm_L, perm_R, Q_R, Q_P, Y, nullptr, workspace,
+                      ws_bytes, stream);
+}
+
+poetx_status poetx_mx4_backward(const poetx_desc* desc, int n_tokens, const void* dY, const void* X,
+                                const uint8_t* codes, const uint8_t* scales, const int32_t* perm_L,
+                                const int32_t* perm_R, const void* Q_R, const void* Q_P, const float* theta_R,
+                                const float* theta_P, void* dX, float* grad_theta_R, float* grad_theta_P,
+                                void* workspace, size_t ws_bytes, poetx_stream stream) {
+  POETX_TRY(check_mx4_layer(desc));
+  POETX_TRY(check_ptrs({codes, scales}));
+  return backward_impl(desc, n_tokens, dY, X, codes, {nullptr, scales}, perm_L, perm_R, Q_R, Q_P, theta_R, theta_P,
+                       nullptr, dX, grad_theta_R, grad_theta_P, workspace, ws_bytes, stream);
+}
+
+poetx_status poetx_mx4_merge(const poetx_desc* desc, uint8_t* codes, uint8_t* scales, const void* Q_R, const void* Q_P,
+                             const int32_t* perm_L_old, const int32_t* perm_R_old, const int32_t* perm_L_new,
+                             const int32_t* perm_R_new, float* theta_R, float* theta_P, void* workspace,
+                             size_t ws_bytes, poetx_stream stream) {
+  POETX_TRY(check_mx4_layer(desc));
+  POETX_TRY(check_ptrs({codes, scales, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new, perm_R_new, theta_R, theta_P}));
+  const MergePlan m = merge_plan(desc);
+  POETX_TRY(check_ws(workspace, ws_bytes, m.total));
+  POETX_TRY(debug_check_perms(stream, {{perm_L_old, desc->d_out}, {perm_R_old, desc->d_in},
+                                       {perm_L_new, desc->d_out}, {perm_R_new, desc->d_in}}));
+  char* ws = static_cast<char*>(workspace);
+  // As poetx_xq_merge: the bf16 weight lives only in the workspace for the call.
+  POETX_TRY(mx4_dequantize(desc->d_out, desc->d_in, codes, scales, ws + m.M2, stream));
+  POETX_TRY(merge_impl(desc, ws + m.M2, ws + m.T, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new, perm_R_new, theta_R,
+                       theta_P, ws, stream));
+  return mx4_quantize(POETX_BF16, desc->d_out, desc->d_in, ws + m.T, codes, scales, stream);
 }
 
 poetx_status poetx_device_status(int* detail) {

@@ -11,7 +11,8 @@ import torch
 from . import (POETX_BF16, POETX_F32, POETX_FAST, POETX_MEM, poetx_absorb, poetx_adamw_cfg, poetx_adamw_reset,
                poetx_adamw_step, poetx_backward, poetx_cnp, poetx_cnp_forward, poetx_desc, poetx_fourperm_backward,
                poetx_fourperm_forward, poetx_fourperm_workspace_size, poetx_forward,
-               poetx_merge, poetx_wc_backward, poetx_wc_forward, poetx_wc_saved_size, poetx_wc_workspace_size,
+               poetx_merge, poetx_mx4_backward, poetx_mx4_forward, poetx_mx4_merge, poetx_mx4_quantize,
+               poetx_wc_backward, poetx_wc_forward, poetx_wc_saved_size, poetx_wc_workspace_size,
                poetx_workspace_size, poetx_xq_backward, poetx_xq_forward, poetx_xq_merge, poetx_xq_quantize)
 
 TORCH_DTYPE = {POETX_F32: torch.float32, POETX_BF16: torch.bfloat16}
@@ -35,8 +36,9 @@ class PoetxLayer:
         P = b * (b - 1) // 2
         dev = self.device
         self.W0p = torch.empty(dout, din, dtype=dt, device=dev)
-        # POET-XQ (after quantize()): W0' as int8 codes W0q [d_out, d_in] and scales W0s [d_out].
-        self.xq = False
+        # POET-XQ (after quantize()): W0' as int8 codes W0q [d_out, d_in] and scales W0s [d_out]; MX4
+        # (after quantize("mx4")): 4-bit codes W0q uint8 [d_out, d_in / 2], scales W0s uint8 [d_out, d_in / 32].
+        self.xq = self.mx4 = False
         self.W0q = self.W0s = None
         # theta_R and theta_P (and their gradients and AdamW moments) are stored back to back so
         # that one optimiser launch covers both sides.
@@ -83,6 +85,9 @@ class PoetxLayer:
         if self.xq:
             poetx_xq_forward(self.desc, self.n, X, self.W0q, self.W0s, self.perm_L, self.perm_R, self.Q_R, self.Q_P,
                              self.Y, self.ws)
+        elif self.mx4:
+            poetx_mx4_forward(self.desc, self.n, X, self.W0q, self.W0s, self.perm_L, self.perm_R, self.Q_R, self.Q_P,
+                              self.Y, self.ws)
         else:
             poetx_forward(self.desc, self.n, X, self.W0p, self.perm_L, self.perm_R, self.Q_R, self.Q_P, self.Y,
                           self.saved, self.ws)
@@ -92,20 +97,36 @@ class PoetxLayer:
         if self.xq:
             poetx_xq_backward(self.desc, self.n, dY, X, self.W0q, self.W0s, self.perm_L, self.perm_R, self.Q_R,
                               self.Q_P, self.theta_R, self.theta_P, self.dX, self.g_R, self.g_P, self.ws)
+        elif self.mx4:
+            poetx_mx4_backward(self.desc, self.n, dY, X, self.W0q, self.W0s, self.perm_L, self.perm_R, self.Q_R,
+                               self.Q_P, self.theta_R, self.theta_P, self.dX, self.g_R, self.g_P, self.ws)
         else:
             poetx_backward(self.desc, self.n, dY, X, self.W0p, self.perm_L, self.perm_R, self.Q_R, self.Q_P,
                            self.theta_R, self.theta_P, self.saved, self.dX, self.g_R, self.g_P, self.ws)
         return self.dX, self.g_R, self.g_P
 
-    def quantize(self):
-        """Switches the layer to POET-XQ (mem mode, bf16): W0' becomes int8 codes with one scale
-        per row, and the bf16 W0' is released."""
+    def quantize(self, bits: str = "int8"):
+        """Switches the layer (mem mode, bf16) to a quantised W0' and releases the bf16 one: "int8"
+        (POET-XQ, one scale per row) or "mx4" (4 bits, one scale per 32 columns)."""
+        if bits not in ("int8", "mx4"):
+            raise ValueError(f"bits: 'int8' or 'mx4', got {bits!r}")
+        if self.xq or self.mx4:
+            raise ValueError("the layer's weight is quantised already")
         d = self.desc
-        self.W0q = torch.empty(d.d_out, d.d_in, dtype=torch.int8, device=self.device)
-        self.W0s = torch.empty(d.d_out, dtype=torch.float32, device=self.device)
-        poetx_xq_quantize(d, self.W0p, self.W0q, self.W0s)
+        if bits == "mx4":
+            if d.dtype != POETX_BF16 or d.mode != POETX_MEM:
+                raise ValueError("an MX4 weight needs a bf16 layer in mem mode")
+            W0q = torch.empty(d.d_out, d.d_in // 2, dtype=torch.uint8, device=self.device)
+            W0s = torch.empty(d.d_out, d.d_in // 32, dtype=torch.uint8, device=self.device)
+            poetx_mx4_quantize(d.dtype, d.d_out, d.d_in, self.W0p, W0q, W0s)
+            self.mx4 = True
+        else:
+            W0q = torch.empty(d.d_out, d.d_in, dtype=torch.int8, device=self.device)
+            W0s = torch.empty(d.d_out, dtype=torch.float32, device=self.device)
+            poetx_xq_quantize(d, self.W0p, W0q, W0s)
+            self.xq = True
+        self.W0q, self.W0s = W0q, W0s
         self.W0p = None  # stream-ordered release: the quantiser has been enqueued before it
-        self.xq = True
 
     def cnp_forward(self, X: torch.Tensor):
         """CNP and layer forward in one library call (the CNP overlaps the input gather)."""
@@ -117,7 +138,7 @@ class PoetxLayer:
         """CNP forward + layer forward + layer backward (incl. the CNP adjoint).  grad_ready (for
         data parallelism, e.g. GradBuckets.layer_done of this layer) is called once the backward
         pass, which writes the packed gradients, has been enqueued."""
-        if self.xq:
+        if self.xq or self.mx4:
             self.cnp()
             self.forward(X)
         else:
@@ -181,6 +202,9 @@ class PoetxLayer:
         if self.xq:
             poetx_xq_merge(self.desc, self.W0q, self.W0s, self.Q_R, self.Q_P, self.perm_L, self.perm_R, pi_L_new,
                            pi_R_new, self.theta_R, self.theta_P, self.ws)
+        elif self.mx4:
+            poetx_mx4_merge(self.desc, self.W0q, self.W0s, self.Q_R, self.Q_P, self.perm_L, self.perm_R, pi_L_new,
+                            pi_R_new, self.theta_R, self.theta_P, self.ws)
         else:
             poetx_merge(self.desc, self.W0p, self.Q_R, self.Q_P, self.perm_L, self.perm_R, pi_L_new, pi_R_new,
                         self.theta_R, self.theta_P, self.ws)

@@ -1,0 +1,455 @@
+"""The 4-bit weight (MX4): quantisation, its product and adjoint, and the layer that runs on it.
+
+Codes, scales and the values they stand for are exact functions of the input, so they are compared bit for
+bit.  The product's factors are exact in float32 (2 by 8 significant bits), so with small integers in X and
+scales near 1 every partial sum is an exact float32 number too, in any order: there Y must be the 64-bit
+result rounded once.  With other values, each of the K products may be cut by 2^-23 of a partial sum, which is
+at most S = sum |w x|, and Y is rounded once by half a step, 2^-8 of its value: |dY| <= 2^-8 |Y| + (K + 8) 2^-23 S (8: the
+parts of a split sum).
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+import orthogonal_equivalence_cnp_b200 as P
+import poetx_inputs as I
+from helpers import TOL, device_clean, rel, to_np
+from orthogonal_equivalence_cnp_b200.layer import PoetxLayer, make_desc
+from orthogonal_equivalence_cnp_b200.optim import MultiAdamW
+
+pytestmark = pytest.mark.gpu
+
+
+def _u8(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _empty(rows, cols):
+    return (torch.full((rows, cols // 2), 0xA5, dtype=torch.uint8, device="cuda"),
+            torch.full((rows, cols // 32), 0x5A, dtype=torch.uint8, device="cuda"))
+
+
+# ------------------------------------------------------------------------ the weight format
+def _special(rows, cols, dtype, seed):
+    rng = np.random.default_rng(seed)
+    W = (rng.standard_normal((rows, cols)) * np.exp2(rng.integers(-12, 4, (rows, 1)))).astype(np.float32)
+    ties = np.array([6, 0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5, -0.25, -0.75, 0.24, 0.26, -6, 7.9, -0.0, 5.01], np.float32)
+    for r, f in ((0, 1.0), (1, 2.0 ** -20), (2, 2.0 ** 60)):
+        if r < rows:
+            W[r, :16] = ties * np.float32(f)
+            W[r, 16:32] = 0
+    if rows > 8:
+        W[3] = 0                                    # zero blocks: scale 0, signs kept
+        W[3, 5] = -0.0
+        W[4, 0], W[5, cols - 1], W[6, 1] = np.nan, np.inf, -np.inf
+        W[7, :32] = np.float32(2.0 ** -133) * np.arange(-16, 16, dtype=np.float32)  # subnormal throughout
+        W[8, :32] = np.float32(3.0e38)              # the largest magnitudes
+        W[8, 0] = np.float32(2.0 ** 127)
+    return I.round_to_bf16(W) if dtype == "bf16" else W
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1, 32), (3, 64), (9, 32), (129, 96), (1000, 1056), (513, 4096)])
+def test_quantize_and_back_bit_exact(dtype, rows, cols):
+    W = _special(rows, cols, dtype, rows + cols)
+    t = torch.from_numpy(W).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    codes, scales = _empty(rows, cols)
+    P.poetx_mx4_quantize(P.POETX_BF16 if dtype == "bf16" else P.POETX_F32, rows, cols, t, codes, scales)
+    back = torch.full((rows, cols), 7.0, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_dequantize(rows, cols, codes, scales, back)
+    torch.cuda.synchronize()
+    device_clean()
+    c, s = O.mx4_quantize(W)
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    ref = O.mx4_dequantize(c, s)
+    assert np.array_equal(to_np(back), ref, equal_nan=True)
+    assert np.array_equal(np.signbit(to_np(back))[np.isfinite(ref)], np.signbit(ref)[np.isfinite(ref)])
+
+
+def test_every_code_at_every_scale_reads_back():
+    # All 16 codes under all 256 scales, quantised weights never reaching the last two.
+    codes = np.tile(np.array([0x10, 0x32, 0x54, 0x76, 0x98, 0xBA, 0xDC, 0xFE] * 2, np.uint8), (256, 1))
+    scales = np.arange(256, dtype=np.uint8)[:, None]
+    back = torch.empty(256, 32, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_dequantize(256, 32, _u8(codes), _u8(scales), back)
+    ref = O.mx4_dequantize(codes, scales)
+    ref[np.abs(ref) >= 2.0 ** 128] *= np.inf
+    got = to_np(back)
+    assert np.array_equal(got, ref, equal_nan=True)
+    assert np.array_equal(np.signbit(got[:255]), np.signbit(ref[:255]))
+
+
+def test_quantize_offsets_past_32_bits():
+    rows, cols = 70000, 32768  # 2.3e9 elements
+    W = torch.zeros(rows, cols, dtype=torch.bfloat16, device="cuda")
+    tail = _special(16, cols, "bf16", 5)
+    W[-16:] = torch.from_numpy(tail).cuda()
+    codes, scales = torch.empty(rows, cols // 2, dtype=torch.uint8, device="cuda"), torch.empty(
+        rows, cols // 32, dtype=torch.uint8, device="cuda")
+    P.poetx_mx4_quantize(P.POETX_BF16, rows, cols, W, codes, scales)
+    c, s = O.mx4_quantize(tail)
+    assert np.array_equal(codes[-16:].cpu().numpy(), c) and np.array_equal(scales[-16:].cpu().numpy(), s)
+    assert not codes[:-16].any().item() and not scales[:-16].any().item()
+    W.fill_(1.0)
+    P.poetx_mx4_dequantize(rows, cols, codes, scales, W)
+    assert np.array_equal(to_np(W[-16:]), O.mx4_dequantize(c, s), equal_nan=True)
+    assert not W[:-16].any().item()
+
+
+# ------------------------------------------------------------------------------ the product
+def _matmul(adjoint, X, codes, scales, d_in, d_out, stream=None):
+    """Y with guard rows behind the last token, which must be left as they were."""
+    n, m = X.shape[0], d_in if adjoint else d_out
+    buf = torch.full((n + 3, m), 1234.0, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_matmul(adjoint, n, d_in, d_out, X, codes, scales, buf[:n], stream)
+    torch.cuda.synchronize()
+    device_clean()
+    assert (buf[n:] == 1234).all().item()
+    return buf[:n]
+
+
+def _integer_problem(n, d_in, d_out, adjoint, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    k = d_out if adjoint else d_in
+    X = torch.randint(-2, 3, (n, k), device="cuda", generator=g).to(torch.bfloat16)
+    codes = torch.randint(0, 256, (d_out, d_in // 2), device="cuda", generator=g).to(torch.uint8)
+    scales = torch.randint(126, 129, (d_out, d_in // 32), device="cuda", generator=g).to(torch.uint8)
+    return X, codes, scales
+
+
+def _weight64(codes, scales):
+    lut = torch.tensor([0.0, 0.5, 1, 1.5, 2, 3, 4, 6], dtype=torch.float64, device="cuda")
+    lut = torch.cat([lut, -lut])
+    c = torch.stack([codes & 15, codes >> 4], 2).view(codes.shape[0], -1)
+    s = torch.exp2(scales.double() - 127).repeat_interleave(32, 1)
+    return lut[c.long()] * s
+
+
+SHAPES = [(32, 8), (32, 128), (64, 136), (96, 1000), (1056, 264), (992, 256), (4096, 512), (320, 4096), (2080, 40)]
+TOKENS = [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 127, 200, 257, 600]
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("d_in,d_out", SHAPES)
+def test_products_of_small_integers_are_exact(adjoint, d_in, d_out):
+    for n in TOKENS:
+        X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, n + d_in)
+        Y = _matmul(adjoint, X, codes, scales, d_in, d_out)
+        W = _weight64(codes, scales)
+        ref = X.double() @ (W if adjoint else W.t())
+        assert torch.equal(Y, ref.to(torch.bfloat16)), (n, (Y.double() - ref).abs().max().item())
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 4096, 14336), (5, 14336, 4096), (40, 4096, 4096), (300, 1056, 1000),
+                                          (2048, 4096, 4096), (2500, 4096, 2056), (4097, 2048, 4096)])
+def test_products_of_activations(adjoint, n, d_in, d_out):
+    g = torch.Generator(device="cuda").manual_seed(n)
+    k = d_out if adjoint else d_in
+    X = torch.randn(n, k, device="cuda", generator=g)
+    X = (X * (1 + 15 * (torch.rand(1, k, device="cuda", generator=g) < 0.01))).to(torch.bfloat16)
+    W = torch.randn(d_out, d_in, device="cuda", generator=g) * 0.02
+    codes, scales = _empty(d_out, d_in)
+    P.poetx_mx4_quantize(P.POETX_F32, d_out, d_in, W, codes, scales)
+    Y = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    W = _weight64(codes, scales)
+    W = W if adjoint else W.t()
+    ref, size = X.double() @ W, X.double().abs() @ W.abs()
+    bound = 2.0 ** -8 * ref.abs() + (k + 8) * 2.0 ** -23 * size
+    assert ((Y.double() - ref).abs() <= bound).all().item()
+    # An elementwise bound that K makes wide, and a norm: one rounding, 2^-8 at most.
+    assert (Y.double() - ref).norm().item() <= 2.0 ** -8 * ref.norm().item()
+    again = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    assert torch.equal(Y, again)
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("n", [1, 12, 40, 300])
+def test_nan_blocks_and_tokens_stay_where_they_are(adjoint, n):
+    d_in, d_out = 320, 200
+    X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, 77 + n)
+    scales[13, 4] = 255                       # row 13, columns 128..159
+    clean = _matmul(adjoint, X, codes, torch.where(scales == 255, 127, scales), d_in, d_out)
+    Y = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    hit = torch.zeros_like(Y, dtype=torch.bool)
+    hit[:, 128:160] = True if adjoint else False
+    if not adjoint:
+        hit[:, 13] = True
+    assert Y[hit].isnan().all().item() and torch.equal(Y[~hit], clean[~hit])
+    # A token with an infinity and one with a NaN: no other row changes.
+    scales[13, 4] = 127
+    clean = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    X2 = X.clone()
+    X2[0, 3] = float("nan")
+    if n > 5:
+        X2[5, 8] = float("inf")
+    Y = _matmul(adjoint, X2, codes, scales, d_in, d_out)
+    rows = torch.ones(n, dtype=torch.bool, device="cuda")
+    rows[0] = False
+    if n > 5:
+        rows[5] = False
+        W = _weight64(codes, scales)
+        inf = X2[5:6].double() @ (W if adjoint else W.t())
+        assert torch.equal(Y[5:6].double().nan_to_num(7.0, 1e300, -1e300), inf.to(torch.bfloat16).double().nan_to_num(7.0, 1e300, -1e300))
+    assert Y[0].isnan().all().item() and torch.equal(Y[rows], clean[rows])
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("n", [3, 50])
+def test_far_scales(adjoint, n):
+    # Scales from the smallest to the largest that values reach: products and sums of one magnitude per block
+    # of outputs, so that they are exact.
+    d_in, d_out = 256, 64
+    for e in (0, 1, 2, 100, 126, 127, 128, 129, 130, 200, 245):
+        X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, e)
+        scales.fill_(e)
+        # Partial results of float32's own range: units of 2^-128 and more are exact while they are not cut to
+        # zero; X of 2^20 keeps the smallest scales' products normal.
+        up = 2.0 ** 20 if e < 64 else 2.0 ** -20 if e > 200 else 1.0
+        Y = _matmul(adjoint, (X * up), codes, scales, d_in, d_out)
+        W = _weight64(codes, scales)
+        ref = (X.double() * up) @ (W if adjoint else W.t())
+        assert torch.equal(Y, ref.to(torch.bfloat16)), e
+
+
+def test_product_offsets_past_32_bits():
+    n, d_in, d_out = 160000, 64, 14336  # 2.3e9 outputs
+    X, codes, scales = _integer_problem(n, d_in, d_out, 0, 3)
+    Y = torch.empty(n, d_out, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_matmul(0, n, d_in, d_out, X, codes, scales, Y)
+    W = _weight64(codes, scales)
+    rows = torch.tensor([0, 77777, 149796, 149797, n - 1], device="cuda")
+    assert torch.equal(Y[rows], (X[rows].double() @ W.t()).to(torch.bfloat16))
+    dX = torch.empty(n, d_in, dtype=torch.bfloat16, device="cuda")
+    dY = (Y > 0).to(torch.bfloat16)
+    P.poetx_mx4_matmul(1, n, d_in, d_out, dY, codes, scales, dX)
+    assert torch.equal(dX[rows], (dY[rows].double() @ W).to(torch.bfloat16))
+    device_clean()
+
+
+def test_products_on_streams_and_in_a_graph():
+    cases = []
+    for i, (adjoint, n, d_in, d_out) in enumerate([(0, 1, 4096, 1024), (0, 33, 1056, 1000), (1, 300, 1056, 1000),
+                                                   (1, 2, 1024, 4096), (0, 700, 512, 2048)]):
+        X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, i)
+        W = _weight64(codes, scales)
+        Y = torch.zeros(n, d_in if adjoint else d_out, dtype=torch.bfloat16, device="cuda")
+        cases.append((adjoint, n, d_in, d_out, X, codes, scales, Y,
+                      (X.double() @ (W if adjoint else W.t())).to(torch.bfloat16)))
+
+    def run(stream=None):
+        for c in cases:
+            P.poetx_mx4_matmul(*c[:8], stream)
+
+    def check():
+        for c in cases:
+            assert torch.equal(c[7], c[8]), c[:4]
+            c[7].zero_()
+
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for c, s in zip(cases, streams):  # all at once
+        P.poetx_mx4_matmul(*c[:8], s)
+    torch.cuda.synchronize()
+    check()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        check()
+    # New inputs in the captured buffers.
+    for c in cases:
+        c[4].neg_()
+    graph.replay()
+    torch.cuda.synchronize()
+    for c in cases:
+        assert torch.equal(c[7], -c[8])
+    device_clean()
+
+
+def test_quantize_then_multiply_needs_no_wait():
+    # Launched back to back on one stream: the product reads what the quantiser has just written.
+    g = torch.Generator(device="cuda").manual_seed(4)
+    codes, scales = _empty(4096, 4096)
+    back = torch.empty(4096, 4096, dtype=torch.bfloat16, device="cuda")
+    for i in range(4):
+        W = (torch.randn(4096, 4096, device="cuda", generator=g) * 2.0 ** -i).to(torch.bfloat16)
+        X = torch.eye(4096, device="cuda", dtype=torch.bfloat16)[i * 40:i * 40 + 37].contiguous()
+        Y = torch.empty(37, 4096, dtype=torch.bfloat16, device="cuda")
+        P.poetx_mx4_quantize(P.POETX_BF16, 4096, 4096, W, codes, scales)
+        P.poetx_mx4_matmul(1, 37, 4096, 4096, X, codes, scales, Y)
+        P.poetx_mx4_dequantize(4096, 4096, codes, scales, back)
+        assert torch.equal(Y, back[i * 40:i * 40 + 37])
+
+
+# -------------------------------------------------------------------------------- the layer
+def _layer(inp, n=None):
+    s = inp.shape
+    L = PoetxLayer(make_desc(s.d_in, s.d_out, s.b, s.k, "bf16", "mem"), n or inp.X.shape[0])
+    L.load_state(inp.W0, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R)
+    L.quantize("mx4")
+    return L
+
+
+def _oracle(inp, theta_R=None, theta_P=None, rows=None):
+    s = inp.shape
+    tR = inp.theta_R if theta_R is None else theta_R
+    tP = inp.theta_P if theta_P is None else theta_P
+    X, dY = (inp.X, inp.dY) if rows is None else (inp.X[rows], inp.dY[rows])
+    codes, scales = O.mx4_quantize(O.absorb(inp.W0, inp.pi_L, inp.pi_R))
+    W = O.mx4_dequantize(codes, scales)
+    Y = O.forward_chain(X, W, O.cnp(tR, s.b, s.k), O.cnp(tP, s.b, s.k), inp.pi_L, inp.pi_R)[0]
+    dX, gR, gP = O.backward_chain(X, dY, W, tR, tP, inp.pi_L, inp.pi_R, s.b, s.k)
+    return dict(Y=Y, dX=dX, g_R=gR, g_P=gP, codes=codes, scales=scales)
+
+
+@pytest.mark.parametrize("d_in,d_out,b,n", [(512, 768, 256, 300), (768, 512, 128, 200), (1024, 1024, 512, 129),
+                                            (64, 192, 64, 1), (512, 512, 256, 600), (256, 1280, 64, 77)])
+def test_layer_matches_oracle(d_in, d_out, b, n):
+    s = I.small_shape(d_in, d_out, b, 3, n, "bf16", "mem", theta_std=0.005, w_std=0.02)
+    inp = I.make_layer(s, 5 * d_in + d_out + b + n)
+    L = _layer(inp)
+    L.step(L.to_dev(inp.X), L.to_dev(inp.dY))
+    torch.cuda.synchronize()
+    device_clean()
+    o = _oracle(inp)
+    assert np.array_equal(L.W0q.cpu().numpy(), o["codes"]) and np.array_equal(L.W0s.cpu().numpy(), o["scales"])
+    errs = {k: rel(to_np(t), o[k]) for k, t in (("Y", L.Y), ("dX", L.dX), ("g_R", L.g_R), ("g_P", L.g_P))}
+    assert all(e <= TOL["bf16"] for e in errs.values()), errs
+
+
+def test_full_size_layer_sampled():
+    inp = I.make_workload("llama8b_up_4096x14336_b256_bf16_mem")
+    rows = np.sort(np.random.default_rng(6).choice(inp.X.shape[0], 64, replace=False))
+    dY = np.zeros_like(inp.dY)
+    dY[rows] = inp.dY[rows]
+    L = _layer(inp)
+    L.step(L.to_dev(inp.X), L.to_dev(dY))
+    torch.cuda.synchronize()
+    device_clean()
+    o = _oracle(inp, rows=rows)
+    errs = {"Y": rel(to_np(L.Y)[rows], o["Y"]), "dX": rel(to_np(L.dX)[rows], o["dX"]),
+            "g_R": rel(to_np(L.g_R), o["g_R"]), "g_P": rel(to_np(L.g_P), o["g_P"])}
+    assert all(e <= TOL["bf16"] for e in errs.values()), errs
+
+
+def test_theta_gradients_match_differences():
+    # The layer's gradient along a random direction of theta against a difference of the oracle's loss
+    # <dY, Y(theta)> in 64 bits (central, so off by the step's square).
+    s = I.small_shape(256, 128, 64, 3, 40, "bf16", "mem", theta_std=0.01, w_std=0.02)
+    inp = I.make_layer(s, 31)
+    L = _layer(inp)
+    L.step(L.to_dev(inp.X), L.to_dev(inp.dY))
+    codes, scales = O.mx4_quantize(O.absorb(inp.W0, inp.pi_L, inp.pi_R))
+    W = O.mx4_dequantize(codes, scales)
+    gR, gP = to_np(L.g_R), to_np(L.g_P)
+    # The gradient's own direction: its size is the product's, and errors elsewhere do not drown it.
+    dR, dP = gR / np.linalg.norm(gR), gP / np.linalg.norm(gP)
+
+    def loss(h, side):
+        tR = inp.theta_R + (h * dR if side == "R" else 0)
+        tP = inp.theta_P + (h * dP if side == "P" else 0)
+        Y = O.forward_chain(inp.X, W, O.cnp(tR, s.b, s.k), O.cnp(tP, s.b, s.k), inp.pi_L, inp.pi_R)[0]
+        return float((inp.dY.astype(np.float64) * Y).sum())
+
+    for side, g in (("R", gR), ("P", gP)):
+        diff = (loss(1e-3, side) - loss(-1e-3, side)) / 2e-3
+        assert abs(diff - np.linalg.norm(g)) <= TOL["bf16"] * np.linalg.norm(g), side
+
+
+@pytest.mark.parametrize("d_in,d_out,b", [(1024, 512, 256), (512, 768, 128)])
+def test_merge(d_in, d_out, b):
+    s = I.small_shape(d_in, d_out, b, 3, 64, "bf16", "mem", theta_std=0.005, w_std=0.02)
+    inp = I.make_layer(s, 91 + b)
+    pL2, pR2 = I.fresh_permutations(s, 91 + b)
+    L = _layer(inp)
+    L.cnp()
+    # The same merge on the bf16 weight that the codes stand for, then quantised, must give the same codes.
+    F = PoetxLayer(L.desc, 64)
+    F.load_state(inp.W0, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R)
+    P.poetx_mx4_dequantize(d_out, d_in, L.W0q, L.W0s, F.W0p)
+    F.cnp()
+    new = torch.from_numpy(pL2).cuda(), torch.from_numpy(pR2).cuda()
+    L.merge(*new)
+    F.merge(*new)
+    merged = to_np(F.W0p)
+    torch.cuda.synchronize()
+    device_clean()
+    assert torch.count_nonzero(L.theta_R).item() == 0 and torch.count_nonzero(L.theta_P).item() == 0
+    codes, scales = O.mx4_quantize(O.absorb(inp.W0, inp.pi_L, inp.pi_R))
+    Wn = O.mx4_merge(codes, scales, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R, pL2, pR2, b, 3)[0]
+    assert rel(merged, Wn) <= TOL["bf16"]
+    cn, sn = O.mx4_quantize(merged)
+    assert np.array_equal(L.W0q.cpu().numpy(), cn) and np.array_equal(L.W0s.cpu().numpy(), sn)
+    # The merged layer serves tokens as a plain product in the permuted basis: Y[:, pi_L] = X[:, pi_R] W0'^T.
+    L.cnp()
+    X = L.to_dev(inp.X)
+    L.forward(X)
+    Z = _matmul(0, X[:, new[1].long()].contiguous(), L.W0q, L.W0s, d_in, d_out)
+    Y = torch.empty_like(Z)
+    Y[:, new[0].long()] = Z
+    assert rel(to_np(L.Y), to_np(Y)) <= TOL["bf16"]
+
+
+def test_training_steps_with_8_bit_moments():
+    # Three steps of the layer on its 4-bit weight with MultiAdamW on e4m3 moments, a captured graph of the
+    # same step replayed for the second and third, against the oracle's steps.
+    s = I.small_shape(512, 384, 128, 3, 96, "bf16", "mem", theta_std=0.005, w_std=0.02)
+    inp = I.make_layer(s, 44)
+    L = _layer(inp)
+    X, dY = L.to_dev(inp.X), L.to_dev(inp.dY)
+    opt = MultiAdamW.from_params([L.theta_R, L.theta_P], [L.g_R, L.g_P])
+    cfg = P.poetx_adamw_cfg(1e-4, 0.5, 0.9, 0.999, 1e-8, 0.0)
+    tR, tP = inp.theta_R.astype(np.float64), inp.theta_P.astype(np.float64)
+    state = [[np.zeros(t.size), np.zeros(t.size)] for t in (tR, tP)]
+    graph = None
+    for t in (1, 2, 3):
+        if graph is None:
+            L.step(X, dY)
+            graph = torch.cuda.CUDAGraph()
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graph):
+                L.step(X, dY)
+        else:
+            graph.replay()
+        o = _oracle(inp, tR, tP)
+        for got, want in ((L.g_R, o["g_R"]), (L.g_P, o["g_P"]), (L.Y, o["Y"]), (L.dX, o["dX"])):
+            assert rel(to_np(got), want) <= TOL["bf16"], t
+        # The oracle's step on the layer's own gradients: the optimiser's part alone.
+        for i, (x, g) in enumerate(((tR, L.g_R), (tP, L.g_P))):
+            m, v = state[i]
+            p, m, v = O.adamw_step(x.ravel(), to_np(g).ravel(), m, v, t, 1e-4, 0.5, 0.9, 0.999, 1e-8, 0.0)
+            qm, um = O.e4m3_moments(m, False)
+            qr, ur = O.e4m3_moments(np.sqrt(v), True)
+            state[i] = [qm * np.repeat(um, 256)[:m.size], (qr * np.repeat(ur, 256)[:m.size]) ** 2]
+            x[...] = p.reshape(x.shape)
+        opt.step(cfg)
+        # A code next to a rounding border may fall on the other side: half a step of m (2^-4) and of the root
+        # (2^-4) of an update of at most lr per step, on few elements; the float32 steps by far less.
+        for got, want, start in ((L.theta_R, tR, inp.theta_R), (L.theta_P, tP, inp.theta_P)):
+            assert rel(to_np(got) - start, want.reshape(got.shape) - start) <= 2.0 ** -4, t
+    device_clean()
+
+
+def test_refusals_and_empty_calls():
+    L = PoetxLayer(make_desc(512, 512, 256, 3, "bf16", "mem"), 8)
+    L.W0p.zero_()
+    L.quantize("mx4")
+    assert L.W0p is None and not L.W0q.any().item() and not L.W0s.any().item()
+    with pytest.raises(ValueError):
+        L.quantize("mx4")
+    with pytest.raises(ValueError):
+        PoetxLayer(make_desc(512, 512, 256, 3, "bf16", "fast"), 8).quantize("mx4")
+    P.poetx_mx4_forward(L.desc, 0, L.dX, L.W0q, L.W0s, L.perm_L, L.perm_R, L.Q_R, L.Q_P, L.Y, L.ws)
+    P.poetx_mx4_matmul(0, 0, 512, 512, L.dX, L.W0q, L.W0s, L.Y)
+    with pytest.raises(ValueError, match="W0q|codes"):
+        P.poetx_mx4_matmul(0, 8, 1024, 512, torch.empty(8, 1024, dtype=torch.bfloat16, device="cuda"), L.W0q, L.W0s, L.Y)
+    with pytest.raises(ValueError, match="X"):
+        P.poetx_mx4_matmul(0, 9, 512, 512, L.dX, L.W0q, L.W0s, torch.empty(9, 512, dtype=torch.bfloat16, device="cuda"))
+    with pytest.raises(ValueError, match="contiguous"):
+        P.poetx_mx4_matmul(0, 4, 512, 512, torch.empty(8, 512, dtype=torch.bfloat16, device="cuda")[::2], L.W0q, L.W0s, L.Y)
+    device_clean()
