@@ -151,6 +151,18 @@ def exported_symbols():
     return sorted(_SIGNATURES)
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported at the first use (the C ABI itself does without it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
 def _ptr(x):
     """Device address of an array argument: a CUDA tensor (contiguous; checked), a raw device
     address (int, the caller's responsibility) or None."""
@@ -206,8 +218,9 @@ def _nbytes(x):
 
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # The raw handle of the current stream: building torch's Stream object for it costs 3 us, more than a launch.
+        torch = _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -377,47 +390,67 @@ def poetx_xq_merge(desc, W0q, W0s, Q_R, Q_P, perm_L_old, perm_R_old, perm_L_new,
                                 _ptr(theta_P), _ptr(workspace), ws_bytes, _stream(stream)), "poetx_xq_merge")
 
 
-def _check_mx4(rows, cols, codes, scales):
-    import torch
-    # Codes of two weights a byte and E8M0 scales, as uint8 or under torch's own names for them.
-    for x, name, numel, own in ((codes, "codes", rows * cols // 2, "float4_e2m1fn_x2"),
-                                (scales, "scales", rows * cols // POETX_MX4_BLOCK, "float8_e8m0fnu")):
-        _need(x, name, numel)
-        if hasattr(x, "dtype") and x.dtype not in (torch.uint8, getattr(torch, own, torch.uint8)):
-            raise ValueError(f"{name}: expected torch.uint8 or torch.{own}, got {x.dtype}")
+def _array(x, name, numel, dtypes, device):
+    """Device address of an array argument (as _ptr), which must hold at least `numel` elements of one of
+    `dtypes` and lie on the current device, where the library launches."""
+    if x is None or isinstance(x, int):
+        return x
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
+    if x.numel() < numel:
+        raise ValueError(f"{name}: needs at least {numel} elements, has {x.numel()}")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: array arguments must be CUDA tensors (or raw device addresses)")
+    if not x.is_contiguous():
+        raise ValueError(f"{name}: array arguments must be contiguous")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on cuda:{x.get_device()}, not on the current device cuda:{device}")
+    return x.data_ptr()
+
+
+_mx4_types = None
+
+
+def _mx4(rows, cols, codes, scales, *others):
+    """Addresses of codes, scales and others (x, name, numel, POETX_ dtype) for one MX4 call.  Codes of two
+    weights a byte and E8M0 scales are uint8, or of torch's own types for them."""
+    global _mx4_types
+    torch = _torch()
+    if _mx4_types is None:
+        _mx4_types = ((torch.uint8, torch.float4_e2m1fn_x2), (torch.uint8, torch.float8_e8m0fnu),
+                      {POETX_BF16: (torch.bfloat16,), POETX_F32: (torch.float32,)})
+    code_types, scale_types, types = _mx4_types
+    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
+    out = [_array(codes, "codes", rows * cols // 2, code_types, dev),
+           _array(scales, "scales", rows * cols // POETX_MX4_BLOCK, scale_types, dev)]
+    for x, name, numel, dtype in others:
+        out.append(_array(x, name, numel, types[dtype], dev))
+    return out
 
 
 def poetx_mx4_quantize(dtype, rows, cols, W, codes, scales, stream=None):
-    import torch
-    _need(W, "W", rows * cols, torch.bfloat16 if dtype == POETX_BF16 else torch.float32)
-    _check_mx4(rows, cols, codes, scales)
-    _check(lib().poetx_mx4_quantize(dtype, rows, cols, _ptr(W), _ptr(codes), _ptr(scales), _stream(stream)),
-           "poetx_mx4_quantize")
+    c, s, w = _mx4(rows, cols, codes, scales, (W, "W", rows * cols, POETX_BF16 if dtype == POETX_BF16 else POETX_F32))
+    _check(lib().poetx_mx4_quantize(dtype, rows, cols, w, c, s, _stream(stream)), "poetx_mx4_quantize")
 
 
 def poetx_mx4_dequantize(rows, cols, codes, scales, W, stream=None):
-    import torch
-    _need(W, "W", rows * cols, torch.bfloat16)
-    _check_mx4(rows, cols, codes, scales)
-    _check(lib().poetx_mx4_dequantize(rows, cols, _ptr(codes), _ptr(scales), _ptr(W), _stream(stream)),
-           "poetx_mx4_dequantize")
+    c, s, w = _mx4(rows, cols, codes, scales, (W, "W", rows * cols, POETX_BF16))
+    _check(lib().poetx_mx4_dequantize(rows, cols, c, s, w, _stream(stream)), "poetx_mx4_dequantize")
 
 
 def poetx_mx4_matmul(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, stream=None):
-    import torch
-    _need(X, "X", n_tokens * (d_out if adjoint else d_in), torch.bfloat16)
-    _need(Y, "Y", n_tokens * (d_in if adjoint else d_out), torch.bfloat16)
-    _check_mx4(d_out, d_in, codes, scales)
-    _check(lib().poetx_mx4_matmul(1 if adjoint else 0, n_tokens, d_in, d_out, _ptr(X), _ptr(codes), _ptr(scales),
-                                  _ptr(Y), _stream(stream)), "poetx_mx4_matmul")
+    c, s, x, y = _mx4(d_out, d_in, codes, scales, (X, "X", n_tokens * (d_out if adjoint else d_in), POETX_BF16),
+                      (Y, "Y", n_tokens * (d_in if adjoint else d_out), POETX_BF16))
+    _check(lib().poetx_mx4_matmul(1 if adjoint else 0, n_tokens, d_in, d_out, x, c, s, y, _stream(stream)),
+           "poetx_mx4_matmul")
 
 
 def poetx_mx4_forward(desc, n_tokens, X, codes, scales, perm_L, perm_R, Q_R, Q_P, Y, workspace, ws_bytes=None,
                       stream=None):
     _check_layer(desc, n_tokens, X=X, perm_L=perm_L, perm_R=perm_R, Q_R=Q_R, Q_P=Q_P, Y=Y)
-    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    c, s = _mx4(desc.d_out, desc.d_in, codes, scales)
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _check(lib().poetx_mx4_forward(ctypes.byref(desc), n_tokens, _ptr(X), _ptr(codes), _ptr(scales), _ptr(perm_L),
+    _check(lib().poetx_mx4_forward(ctypes.byref(desc), n_tokens, _ptr(X), c, s, _ptr(perm_L),
                                    _ptr(perm_R), _ptr(Q_R), _ptr(Q_P), _ptr(Y), _ptr(workspace), ws_bytes,
                                    _stream(stream)), "poetx_mx4_forward")
 
@@ -426,9 +459,9 @@ def poetx_mx4_backward(desc, n_tokens, dY, X, codes, scales, perm_L, perm_R, Q_R
                        grad_theta_R, grad_theta_P, workspace, ws_bytes=None, stream=None):
     _check_layer(desc, n_tokens, dY=dY, X=X, perm_L=perm_L, perm_R=perm_R, Q_R=Q_R, Q_P=Q_P, theta_R=theta_R,
                  theta_P=theta_P, dX=dX, grad_theta_R=grad_theta_R, grad_theta_P=grad_theta_P)
-    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    c, s = _mx4(desc.d_out, desc.d_in, codes, scales)
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _check(lib().poetx_mx4_backward(ctypes.byref(desc), n_tokens, _ptr(dY), _ptr(X), _ptr(codes), _ptr(scales),
+    _check(lib().poetx_mx4_backward(ctypes.byref(desc), n_tokens, _ptr(dY), _ptr(X), c, s,
                                     _ptr(perm_L), _ptr(perm_R), _ptr(Q_R), _ptr(Q_P), _ptr(theta_R), _ptr(theta_P),
                                     _ptr(dX), _ptr(grad_theta_R), _ptr(grad_theta_P), _ptr(workspace), ws_bytes,
                                     _stream(stream)), "poetx_mx4_backward")
@@ -438,9 +471,9 @@ def poetx_mx4_merge(desc, codes, scales, Q_R, Q_P, perm_L_old, perm_R_old, perm_
                     workspace, ws_bytes=None, stream=None):
     _check_layer(desc, Q_R=Q_R, Q_P=Q_P, perm_L_old=perm_L_old, perm_R_old=perm_R_old, perm_L_new=perm_L_new,
                  perm_R_new=perm_R_new, theta_R=theta_R, theta_P=theta_P)
-    _check_mx4(desc.d_out, desc.d_in, codes, scales)
+    c, s = _mx4(desc.d_out, desc.d_in, codes, scales)
     ws_bytes = _nbytes(workspace) if ws_bytes is None else ws_bytes
-    _check(lib().poetx_mx4_merge(ctypes.byref(desc), _ptr(codes), _ptr(scales), _ptr(Q_R), _ptr(Q_P), _ptr(perm_L_old),
+    _check(lib().poetx_mx4_merge(ctypes.byref(desc), c, s, _ptr(Q_R), _ptr(Q_P), _ptr(perm_L_old),
                                  _ptr(perm_R_old), _ptr(perm_L_new), _ptr(perm_R_new), _ptr(theta_R), _ptr(theta_P),
                                  _ptr(workspace), ws_bytes, _stream(stream)), "poetx_mx4_merge")
 

@@ -63,17 +63,27 @@ def test_binding_checks_types_and_sizes():
     class Fake:
         is_cuda = True
 
-        def __init__(self, n, dtype):
-            self.n, self.dtype = n, dtype
+        def __init__(self, n, dtype, dev=0):
+            self.n, self.dtype, self.dev = n, dtype, dev
 
         def numel(self):
             return self.n
+
+        def is_contiguous(self):
+            return True
+
+        def get_device(self):
+            return self.dev
+
+        def data_ptr(self):
+            return A
 
     bf, u8 = torch.bfloat16, torch.uint8
     good = dict(W=Fake(64 * 4, bf), codes=Fake(64 * 2, u8), scales=Fake(8, u8))
     for kw, word in ((dict(W=Fake(255, bf)), "W"), (dict(W=Fake(256, torch.float32)), "W"), (dict(codes=Fake(127, u8)), "codes"),
                      (dict(codes=Fake(128, torch.int8)), "codes"), (dict(scales=Fake(7, u8)), "scales"),
-                     (dict(scales=Fake(8, torch.float32)), "scales")):
+                     (dict(scales=Fake(8, torch.float32)), "scales"), (dict(codes=Fake(128, u8, 1)), "current device"),
+                     (dict(W=torch.zeros(4, 64, dtype=bf)), "CUDA")):
         a = dict(good, **kw)
         with pytest.raises(ValueError, match=word):
             P.poetx_mx4_quantize(P.POETX_BF16, 4, 64, a["W"], a["codes"], a["scales"], 0)
