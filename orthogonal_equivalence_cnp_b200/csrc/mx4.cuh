@@ -110,7 +110,255 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
     W[i] = mx4_decode8(codes[i], mx4_scale(scales[i >> 2]));
 }
 
-// -------------------------------------------------------------------------------- product
+// ------------------------------------------------------------------- product, few tokens
+// A word of four nibbles in each half (bits 4i..4i+3) to four bf16x2: result i holds nibble i of both
+// halves, times f1.  Masked, a nibble s e e m times 2^6 + 2^12 puts e e m at a bf16's lowest exponent and
+// highest mantissa bits and s at its sign.  Integer logic runs at half the rate of multiplications here and
+// is what bounds the kernels below, hence the multiplication in place of two shifts: 9 logic operations for
+// eight weights (mx4_decode8, which keeps the columns' order, takes 17).
+__device__ __forceinline__ void mx4_nibbles(uint32_t p, uint32_t f1, uint32_t (&o)[4]) {
+  const uint32_t q = p >> 8;
+  o[0] = bf16x2_mul(((p & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
+  o[1] = bf16x2_mul(((p & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
+  o[2] = bf16x2_mul(((q & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
+  o[3] = bf16x2_mul(((q & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Up to 8 NT tokens.  The product is bound by reading the codes once (and by decoding them), so nothing is
+// staged: every thread loads codes straight into the registers that the warp-level tensor instruction takes
+// them from.  The order of the K index inside an instruction is free as long as both operands agree, so a
+// thread takes the K positions whose codes lie together in memory.  The warps of a block, and the blocks of a
+// cluster, split K and add their sums in shared memory in a fixed order.
+struct Mx4FewArgs {
+  int M, N, K;  // features out, tokens, features in
+  int splits;   // CTAs of a cluster, along K
+  const __nv_bfloat16* X;
+  const uint8_t* codes;
+  const uint8_t* scales;
+  __nv_bfloat16* Y;
+};
+constexpr int MX4_FEW_WARPS = 8;
+constexpr int MX4_FEW_RT = 2;                          // forward: 16-row tiles per block
+constexpr int MX4_FEW_ROWS = 16 * MX4_FEW_RT;          // features of a forward block
+constexpr int MX4_FEW_COLS = 128;                      // features of an adjoint block
+__host__ __device__ constexpr size_t mx4_few_smem(int features, int nt) {
+  return (size_t)MX4_FEW_WARPS * features * 8 * nt * sizeof(float);
+}
+
+// Sums red[warp][token][feature] over the warps and the cluster, rounds once, stores.
+template <int F, int T>
+__device__ __forceinline__ void mx4_few_finish(const Mx4FewArgs& a, float* red, int m0, int split) {
+  using namespace sm100;
+  __syncthreads();
+  for (int e = threadIdx.x; e < F * T; e += MX4_FEW_WARPS * 32) {
+    float x = red[e];
+#pragma unroll
+    for (int w = 1; w < MX4_FEW_WARPS; ++w) x += red[w * F * T + e];
+    red[e] = x;
+  }
+  if (a.splits > 1) cluster_sync_all(); else __syncthreads();
+  const int share = F * T / a.splits;
+  for (int e = split * share + threadIdx.x; e < (split + 1) * share; e += MX4_FEW_WARPS * 32) {
+    const int n = e / F, m = m0 + e % F;
+    if (n < a.N && m < a.M) {
+      float x;
+      if (a.splits > 1) {
+        x = 0.f;
+        for (int r = 0; r < a.splits; ++r) x += ld_cluster_f32(mapa_shared(smem_u32(red + e), (uint32_t)r));
+      } else {
+        x = red[e];
+      }
+      a.Y[(size_t)n * a.M + m] = __float2bfloat16_rn(x);
+    }
+  }
+  if (a.splits > 1) cluster_sync_all();  // the peers have read this block's sums
+}
+
+// Forward: 32 features a block; a warp takes 128 input features at a time, thread (g, t) = (lane / 4, lane % 4) the
+// 32 codes (one scale) of rows g, g + 8, .. at 32 t, and token g's 32 values there.
+template <int NT>
+__global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_forward(const Mx4FewArgs a) {
+  using namespace sm100;
+  extern __shared__ float red[];
+  constexpr int RT = MX4_FEW_RT;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_ROWS;
+  const int nb = (a.K + 127) / 128;
+  const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
+  float acc[RT][NT][4] = {};
+  griddep_wait();
+  const uint8_t* code_at[2 * RT];
+  const uint8_t* scale_at[2 * RT];
+  bool live[2 * RT];
+#pragma unroll
+  for (int r = 0; r < 2 * RT; ++r) {
+    const int m = m0 + 8 * r + g;
+    live[r] = m < a.M;
+    code_at[r] = a.codes + (size_t)m * (a.K / 2) + 16 * t;
+    scale_at[r] = a.scales + (size_t)m * (a.K / 32) + t;
+  }
+  const __nv_bfloat16* x_at[NT];
+  bool has[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    has[u] = 8 * u + g < a.N;
+    x_at[u] = a.X + (size_t)(8 * u + g) * a.K + 32 * t;
+  }
+#pragma unroll 2
+  for (int b = b_lo + warp; b < b_hi; b += MX4_FEW_WARPS) {
+    const bool in = b * 128 + 32 * t < a.K;  // K is a multiple of 32
+    uint4 c[2 * RT];
+    uint32_t e[2 * RT];
+    uint4 x[NT][4];
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r) {
+      c[r] = in && live[r] ? __ldg(reinterpret_cast<const uint4*>(code_at[r] + (size_t)b * 64)) : make_uint4(0, 0, 0, 0);
+      e[r] = in && live[r] ? (uint32_t)__ldg(scale_at[r] + (size_t)b * 4) : 127u;
+    }
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        x[u][i] = in && has[u] ? __ldg(reinterpret_cast<const uint4*>(x_at[u] + (size_t)b * 128) + i) : make_uint4(0, 0, 0, 0);
+    Mx4Scale s[2 * RT];
+    bool two = false;
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r) {
+      s[r] = mx4_scale(e[r]);
+      two |= s[r].two;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint32_t w[2 * RT][4];
+#pragma unroll
+      for (int r = 0; r < 2 * RT; ++r)
+        mx4_nibbles(i == 0 ? c[r].x : i == 1 ? c[r].y : i == 2 ? c[r].z : c[r].w, s[r].f1, w[r]);
+      if (two) {
+#pragma unroll
+        for (int r = 0; r < 2 * RT; ++r)
+          if (s[r].two)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[r][j] = bf16x2_mul(w[r][j], s[r].f2);
+      }
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        // Pairs of K positions j and j + 4, as the codes' halves have them.
+        const uint4 v = x[u][i];
+        const uint32_t y[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
+                               __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+            mma_16816(acc[r][u], w[2 * r][2 * h], w[2 * r + 1][2 * h], w[2 * r][2 * h + 1], w[2 * r + 1][2 * h + 1],
+                      y[2 * h], y[2 * h + 1]);
+      }
+    }
+  }
+  griddep_launch();
+  constexpr int F = MX4_FEW_ROWS, T = 8 * NT;
+  float* out = red + (size_t)warp * F * T;
+#pragma unroll
+  for (int r = 0; r < RT; ++r)
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        out[(8 * u + 2 * t + (q & 1)) * F + 16 * r + 8 * (q >> 1) + g] = acc[r][u][q];
+  mx4_few_finish<F, T>(a, red, m0, split);
+}
+
+// Adjoint: 128 features a block; a warp takes 16 rows of the weight at a time, thread (g, t) the codes of 16
+// features at 16 g in rows 4 t .. 4 t + 3, and token g's four values there.
+template <int NT>
+__global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_adjoint(const Mx4FewArgs a) {
+  using namespace sm100;
+  extern __shared__ float red[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_COLS;
+  const int nb = (a.K + 15) / 16;
+  const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
+  float acc[8][NT][4] = {};
+  griddep_wait();
+  const bool live = m0 + 16 * g < a.M;  // M is a multiple of 32
+  const size_t pitch = (size_t)a.M / 2, spitch = (size_t)a.M / 32;
+  const uint8_t* code_at = a.codes + (size_t)(4 * t) * pitch + m0 / 2 + 8 * g;
+  const uint8_t* scale_at = a.scales + (size_t)(4 * t) * spitch + (m0 + 16 * g) / 32;
+  const __nv_bfloat16* x_at[NT];
+  bool has[NT];
+#pragma unroll
+  for (int u = 0; u < NT; ++u) {
+    has[u] = 8 * u + g < a.N;
+    x_at[u] = a.X + (size_t)(8 * u + g) * a.K + 4 * t;
+  }
+#pragma unroll 2
+  for (int b = b_lo + warp; b < b_hi; b += MX4_FEW_WARPS) {
+    const bool in = b * 16 + 4 * t < a.K;  // K is a multiple of 8
+    uint2 c[4];
+    uint32_t e[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const size_t row = (size_t)b * 16 + r;
+      c[r] = in && live ? __ldg(reinterpret_cast<const uint2*>(code_at + row * pitch)) : make_uint2(0, 0);
+      e[r] = in && live ? (uint32_t)__ldg(scale_at + row * spitch) : 127u;
+    }
+    uint2 x[NT];
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+      x[u] = in && has[u] ? __ldg(reinterpret_cast<const uint2*>(x_at[u] + (size_t)b * 16)) : make_uint2(0, 0);
+    // Rows in pairs, the lower one in the low halves.
+    uint32_t f1[2], f2[2];
+    bool two = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const Mx4Scale lo = mx4_scale(e[2 * h]), hi = mx4_scale(e[2 * h + 1]);
+      f1[h] = __byte_perm(lo.f1, hi.f1, 0x5410);
+      f2[h] = __byte_perm(lo.two ? lo.f2 : 0x3F803F80u, hi.two ? hi.f2 : 0x3F803F80u, 0x5410);
+      two |= lo.two || hi.two;
+    }
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {  // nibbles 0..3, 4..7 of the words
+      const uint32_t sel = v == 0 ? 0x5410u : 0x7632u;
+      uint32_t w[2][2][4];  // [word][pair of rows][nibble]
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          mx4_nibbles(__byte_perm(q ? c[2 * h].y : c[2 * h].x, q ? c[2 * h + 1].y : c[2 * h + 1].x, sel), f1[h], w[q][h]);
+          if (two)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[q][h][j] = bf16x2_mul(w[q][h][j], f2[h]);
+        }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int u = 0; u < NT; ++u)
+          mma_16816(acc[4 * v + j][u], w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j], x[u].x, x[u].y);
+    }
+  }
+  griddep_launch();
+  constexpr int F = MX4_FEW_COLS, T = 8 * NT;
+  float* out = red + (size_t)warp * F * T;
+  // Accumulator row g of product j is feature 16 g + j, row g + 8 feature 16 g + 8 + j.
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        out[(8 * u + 2 * t + (q & 1)) * F + 16 * g + 8 * (q >> 1) + j] = acc[j][u][q];
+  mx4_few_finish<F, T>(a, red, m0, split);
+}
+
+// -------------------------------------------------------------------------------- product, many tokens
 // Y[t][m] = sum_k w(m, k) X[t][k] with w(m, k) = W[m][k] (forward: m an output, k an input feature) or W[k][m]
 // (adjoint), X and Y bf16, sums in fp32.
 //

@@ -578,12 +578,59 @@ poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes
   return last_launch();
 }
 
+template <int NT, bool ADJ>
+poetx_status launch_mx4_few(const Mx4FewArgs& a, cudaStream_t st, int cls) {
+  static bool attr_done[kMaxDevices] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
+  auto kern = ADJ ? mx4_few_adjoint<NT> : mx4_few_forward<NT>;
+  constexpr int features = ADJ ? MX4_FEW_COLS : MX4_FEW_ROWS;
+  constexpr size_t smem = mx4_few_smem(features, NT);
+  if (!attr_done[dev]) {
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+      return POETX_ERR_CUDA;
+    attr_done[dev] = true;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((a.M + features - 1) / features * a.splits), 1, 1);
+  cfg.blockDim = dim3(MX4_FEW_WARPS * 32, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)a.splits;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = a.splits > 1 ? 2 : 1;
+  LaunchScope ls(cls, st);
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return POETX_ERR_CUDA;
+  return last_launch();
+}
+
+constexpr int kMx4Few = 16;  // tokens up to which the product is read-bound: the kernels for few tokens
+
 // Y [n, M] = X [n, K] . W^T (forward: M = d_out, K = d_in) or X . W (adjoint: M = d_in, K = d_out)
 // with W [d_out, d_in] in MX4.  Checked by the callers: aligned pointers, d_in a multiple of 32,
 // d_out of 8.
 poetx_status mx4_product(bool adjoint, int n, int d_in, int d_out, const void* X, const uint8_t* codes,
                          const uint8_t* scales, void* Y, cudaStream_t st, int cls) {
   const int M = adjoint ? d_in : d_out, K = adjoint ? d_out : d_in;
+  if (n <= kMx4Few) {
+    const int features = adjoint ? MX4_FEW_COLS : MX4_FEW_ROWS;
+    const long tiles = ((long)M + features - 1) / features, blocks = (K + (adjoint ? 15 : 127)) / (adjoint ? 16 : 128);
+    Mx4FewArgs a;
+    a.M = M; a.N = n; a.K = K;
+    a.X = static_cast<const __nv_bfloat16*>(X); a.codes = codes; a.scales = scales;
+    a.Y = static_cast<__nv_bfloat16*>(Y);
+    // Split K over a cluster while that leaves every SM at most three blocks and every warp some work.
+    a.splits = 1;
+    while (a.splits < 8 && tiles * a.splits * 2 <= 3L * kNumSms && blocks >= 2L * MX4_FEW_WARPS * a.splits) a.splits *= 2;
+    if (adjoint) return n <= 8 ? launch_mx4_few<1, true>(a, st, cls) : launch_mx4_few<2, true>(a, st, cls);
+    return n <= 8 ? launch_mx4_few<1, false>(a, st, cls) : launch_mx4_few<2, false>(a, st, cls);
+  }
   const Mx4Plan p = mx4_plan(M, n, K);
   if ((n + (long)p.tn - 1) / p.tn > 65535) return POETX_ERR_UNSUPPORTED_SHAPE;
   const Operand x = view(X, n, K, K), c = view(codes, d_out, d_in / 2, d_in / 2);
