@@ -7,6 +7,8 @@
 
 #include <cuda_fp4.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "sm100.cuh"
 
@@ -145,28 +147,30 @@ struct Mx4FewArgs {
   const uint8_t* scales;
   __nv_bfloat16* Y;
 };
-constexpr int MX4_FEW_WARPS = 8;
-constexpr int MX4_FEW_RT = 2;                          // forward: 16-row tiles per block
-constexpr int MX4_FEW_ROWS = 16 * MX4_FEW_RT;          // features of a forward block
-constexpr int MX4_FEW_COLS = 128;                      // features of an adjoint block
-__host__ __device__ constexpr size_t mx4_few_smem(int features, int nt) {
-  return (size_t)MX4_FEW_WARPS * features * 8 * nt * sizeof(float);
+constexpr int MX4_FEW_RT = 2;                   // forward: 16-row tiles per block
+constexpr int MX4_FEW_ROWS = 16 * MX4_FEW_RT;   // features of a forward block
+constexpr int MX4_FEW_COLS = 128;               // features of an adjoint block
+// Warps of a block.  One token, 4096 x 14336: forward 12.7 us with 4 warps and 4 blocks per SM, 13.5 with 8 and 2,
+// 14.9 with 16 rows a block; adjoint 17.7 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
+__host__ __device__ constexpr int mx4_few_warps(bool adj) { return adj ? 8 : 4; }
+__host__ __device__ constexpr size_t mx4_few_smem(bool adj, int nt) {
+  return (size_t)mx4_few_warps(adj) * (adj ? MX4_FEW_COLS : MX4_FEW_ROWS) * 8 * nt * sizeof(float);
 }
 
 // Sums red[warp][token][feature] over the warps and the cluster, rounds once, stores.
-template <int F, int T>
+template <int F, int T, int WARPS>
 __device__ __forceinline__ void mx4_few_finish(const Mx4FewArgs& a, float* red, int m0, int split) {
   using namespace sm100;
   __syncthreads();
-  for (int e = threadIdx.x; e < F * T; e += MX4_FEW_WARPS * 32) {
+  for (int e = threadIdx.x; e < F * T; e += WARPS * 32) {
     float x = red[e];
 #pragma unroll
-    for (int w = 1; w < MX4_FEW_WARPS; ++w) x += red[w * F * T + e];
+    for (int w = 1; w < WARPS; ++w) x += red[w * F * T + e];
     red[e] = x;
   }
   if (a.splits > 1) cluster_sync_all(); else __syncthreads();
   const int share = F * T / a.splits;
-  for (int e = split * share + threadIdx.x; e < (split + 1) * share; e += MX4_FEW_WARPS * 32) {
+  for (int e = split * share + threadIdx.x; e < (split + 1) * share; e += WARPS * 32) {
     const int n = e / F, m = m0 + e % F;
     if (n < a.N && m < a.M) {
       float x;
@@ -185,73 +189,90 @@ __device__ __forceinline__ void mx4_few_finish(const Mx4FewArgs& a, float* red, 
 // Forward: 32 features a block; a warp takes 128 input features at a time, thread (g, t) = (lane / 4, lane % 4) the
 // 32 codes (one scale) of rows g, g + 8, .. at 32 t, and token g's 32 values there.
 template <int NT>
-__global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_forward(const Mx4FewArgs a) {
+__global__ void __launch_bounds__(mx4_few_warps(false) * 32, 4) mx4_few_forward(const Mx4FewArgs a) {
   using namespace sm100;
   extern __shared__ float red[];
-  constexpr int RT = MX4_FEW_RT;
+  constexpr int RT = MX4_FEW_RT, WARPS = mx4_few_warps(false);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_ROWS;
   const int nb = (a.K + 127) / 128;
   const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
   float acc[RT][NT][4] = {};
   griddep_wait();
+  // Rows and tokens past the end repeat the last one: what they give is never stored.
   const uint8_t* code_at[2 * RT];
   const uint8_t* scale_at[2 * RT];
-  bool live[2 * RT];
 #pragma unroll
   for (int r = 0; r < 2 * RT; ++r) {
-    const int m = m0 + 8 * r + g;
-    live[r] = m < a.M;
+    const int m = min(m0 + 8 * r + g, a.M - 1);
     code_at[r] = a.codes + (size_t)m * (a.K / 2) + 16 * t;
     scale_at[r] = a.scales + (size_t)m * (a.K / 32) + t;
   }
   const __nv_bfloat16* x_at[NT];
-  bool has[NT];
 #pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    has[u] = 8 * u + g < a.N;
-    x_at[u] = a.X + (size_t)(8 * u + g) * a.K + 32 * t;
-  }
-#pragma unroll 2
-  for (int b = b_lo + warp; b < b_hi; b += MX4_FEW_WARPS) {
-    const bool in = b * 128 + 32 * t < a.K;  // K is a multiple of 32
-    uint4 c[2 * RT];
+  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(8 * u + g, a.N - 1) * a.K + 32 * t;
+  constexpr bool X_AHEAD = NT == 1;  // registers for 16 tokens' values are only there once
+  struct Block {
+    uint4 c[2 * RT], x[NT][4];
     uint32_t e[2 * RT];
-    uint4 x[NT][4];
-#pragma unroll
-    for (int r = 0; r < 2 * RT; ++r) {
-      c[r] = in && live[r] ? __ldg(reinterpret_cast<const uint4*>(code_at[r] + (size_t)b * 64)) : make_uint4(0, 0, 0, 0);
-      e[r] = in && live[r] ? (uint32_t)__ldg(scale_at[r] + (size_t)b * 4) : 127u;
-    }
+  };
+  auto load_x = [&](Block& k, int b) {
 #pragma unroll
     for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        x[u][i] = in && has[u] ? __ldg(reinterpret_cast<const uint4*>(x_at[u] + (size_t)b * 128) + i) : make_uint4(0, 0, 0, 0);
-    Mx4Scale s[2 * RT];
-    bool two = false;
+      for (int i = 0; i < 4; ++i) k.x[u][i] = __ldg(reinterpret_cast<const uint4*>(x_at[u] + (size_t)b * 128) + i);
+  };
+  auto load = [&](Block& k, int b) {
 #pragma unroll
     for (int r = 0; r < 2 * RT; ++r) {
-      s[r] = mx4_scale(e[r]);
-      two |= s[r].two;
+      k.c[r] = __ldg(reinterpret_cast<const uint4*>(code_at[r] + (size_t)b * 64));
+      k.e[r] = __ldg(scale_at[r] + (size_t)b * 4);
+    }
+    if (X_AHEAD) load_x(k, b);
+  };
+  // The last block of a K that 128 does not divide: threads past the end (K is a multiple of 32) multiply zeros.
+  auto load_end = [&](Block& k, int b) {
+    if (b * 128 + 32 * t < a.K) {
+      load(k, b);
+      if (!X_AHEAD) load_x(k, b);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 2 * RT; ++r) {
+        k.c[r] = make_uint4(0, 0, 0, 0);
+        k.e[r] = 127u;
+      }
+#pragma unroll
+      for (int u = 0; u < NT; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) k.x[u][i] = make_uint4(0, 0, 0, 0);
+    }
+  };
+  auto multiply = [&](const Block& k, auto far) {
+    uint32_t f1[2 * RT], f2[2 * RT];
+#pragma unroll
+    for (int r = 0; r < 2 * RT; ++r) {
+      if (far.value) {
+        const Mx4Scale s = mx4_scale(k.e[r]);
+        f1[r] = s.f1;
+        f2[r] = s.two ? s.f2 : 0x3F803F80u;
+      } else {
+        f1[r] = (k.e[r] + 126u) * 0x00800080u;
+      }
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t w[2 * RT][4];
 #pragma unroll
-      for (int r = 0; r < 2 * RT; ++r)
-        mx4_nibbles(i == 0 ? c[r].x : i == 1 ? c[r].y : i == 2 ? c[r].z : c[r].w, s[r].f1, w[r]);
-      if (two) {
+      for (int r = 0; r < 2 * RT; ++r) {
+        mx4_nibbles(i == 0 ? k.c[r].x : i == 1 ? k.c[r].y : i == 2 ? k.c[r].z : k.c[r].w, f1[r], w[r]);
+        if (far.value)
 #pragma unroll
-        for (int r = 0; r < 2 * RT; ++r)
-          if (s[r].two)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[r][j] = bf16x2_mul(w[r][j], s[r].f2);
+          for (int j = 0; j < 4; ++j) w[r][j] = bf16x2_mul(w[r][j], f2[r]);
       }
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
         // Pairs of K positions j and j + 4, as the codes' halves have them.
-        const uint4 v = x[u][i];
+        const uint4 v = k.x[u][i];
         const uint32_t y[4] = {__byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632),
                                __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632)};
 #pragma unroll
@@ -262,6 +283,33 @@ __global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_forward(const M
                       y[2 * h], y[2 * h + 1]);
       }
     }
+  };
+  auto use = [&](const Block& k) {
+    uint32_t top = k.e[0];
+#pragma unroll
+    for (int r = 1; r < 2 * RT; ++r) top = max(top, k.e[r]);
+    if (__any_sync(0xffffffffu, top > 128u)) multiply(k, std::true_type()); else multiply(k, std::false_type());
+  };
+  // The next block is on its way while one is multiplied.
+  const int b_full = min(b_hi, a.K / 128);
+  Block k0, k1;
+  int b = b_lo + warp;
+  if (b < b_full) load(k0, b);
+#pragma unroll 1
+  while (b < b_full) {
+    if (!X_AHEAD) load_x(k0, b);
+    if (b + WARPS < b_full) load(k1, b + WARPS);
+    use(k0);
+    b += WARPS;
+    if (b >= b_full) break;
+    if (!X_AHEAD) load_x(k1, b);
+    if (b + WARPS < b_full) load(k0, b + WARPS);
+    use(k1);
+    b += WARPS;
+  }
+  if (b < b_hi) {
+    load_end(k0, b);
+    use(k0);
   }
   griddep_launch();
   constexpr int F = MX4_FEW_ROWS, T = 8 * NT;
@@ -273,56 +321,70 @@ __global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_forward(const M
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         out[(8 * u + 2 * t + (q & 1)) * F + 16 * r + 8 * (q >> 1) + g] = acc[r][u][q];
-  mx4_few_finish<F, T>(a, red, m0, split);
+  mx4_few_finish<F, T, WARPS>(a, red, m0, split);
 }
 
 // Adjoint: 128 features a block; a warp takes 16 rows of the weight at a time, thread (g, t) the codes of 16
 // features at 16 g in rows 4 t .. 4 t + 3, and token g's four values there.
 template <int NT>
-__global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_adjoint(const Mx4FewArgs a) {
+__global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(const Mx4FewArgs a) {
   using namespace sm100;
   extern __shared__ float red[];
+  constexpr int WARPS = mx4_few_warps(true);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_COLS;
   const int nb = (a.K + 15) / 16;
   const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
   float acc[8][NT][4] = {};
   griddep_wait();
-  const bool live = m0 + 16 * g < a.M;  // M is a multiple of 32
+  // Features (a multiple of 32) and tokens past the end repeat the last ones: what they give is never stored.
+  const int mg = min(m0 + 16 * g, a.M - 16);
   const size_t pitch = (size_t)a.M / 2, spitch = (size_t)a.M / 32;
-  const uint8_t* code_at = a.codes + (size_t)(4 * t) * pitch + m0 / 2 + 8 * g;
-  const uint8_t* scale_at = a.scales + (size_t)(4 * t) * spitch + (m0 + 16 * g) / 32;
+  const uint8_t* code_at = a.codes + (size_t)(4 * t) * pitch + mg / 2;
+  const uint8_t* scale_at = a.scales + (size_t)(4 * t) * spitch + mg / 32;
   const __nv_bfloat16* x_at[NT];
-  bool has[NT];
 #pragma unroll
-  for (int u = 0; u < NT; ++u) {
-    has[u] = 8 * u + g < a.N;
-    x_at[u] = a.X + (size_t)(8 * u + g) * a.K + 4 * t;
-  }
-#pragma unroll 2
-  for (int b = b_lo + warp; b < b_hi; b += MX4_FEW_WARPS) {
-    const bool in = b * 16 + 4 * t < a.K;  // K is a multiple of 8
-    uint2 c[4];
+  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(8 * u + g, a.N - 1) * a.K + 4 * t;
+  struct Block {
+    uint2 c[4], x[NT];
     uint32_t e[4];
+  };
+  auto load = [&](Block& k, int b) {
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
       const size_t row = (size_t)b * 16 + r;
-      c[r] = in && live ? __ldg(reinterpret_cast<const uint2*>(code_at + row * pitch)) : make_uint2(0, 0);
-      e[r] = in && live ? (uint32_t)__ldg(scale_at + row * spitch) : 127u;
+      k.c[r] = __ldg(reinterpret_cast<const uint2*>(code_at + row * pitch));
+      k.e[r] = __ldg(scale_at + row * spitch);
     }
-    uint2 x[NT];
 #pragma unroll
-    for (int u = 0; u < NT; ++u)
-      x[u] = in && has[u] ? __ldg(reinterpret_cast<const uint2*>(x_at[u] + (size_t)b * 16)) : make_uint2(0, 0);
+    for (int u = 0; u < NT; ++u) k.x[u] = __ldg(reinterpret_cast<const uint2*>(x_at[u] + (size_t)b * 16));
+  };
+  // The last eight rows of a K that 16 does not divide: the other threads multiply zeros.
+  auto load_end = [&](Block& k, int b) {
+    if (b * 16 + 4 * t < a.K) {
+      load(k, b);
+    } else {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        k.c[r] = make_uint2(0, 0);
+        k.e[r] = 127u;
+      }
+#pragma unroll
+      for (int u = 0; u < NT; ++u) k.x[u] = make_uint2(0, 0);
+    }
+  };
+  auto multiply = [&](const Block& k, auto far) {
     // Rows in pairs, the lower one in the low halves.
     uint32_t f1[2], f2[2];
-    bool two = false;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const Mx4Scale lo = mx4_scale(e[2 * h]), hi = mx4_scale(e[2 * h + 1]);
-      f1[h] = __byte_perm(lo.f1, hi.f1, 0x5410);
-      f2[h] = __byte_perm(lo.two ? lo.f2 : 0x3F803F80u, hi.two ? hi.f2 : 0x3F803F80u, 0x5410);
-      two |= lo.two || hi.two;
+      if (far.value) {
+        const Mx4Scale lo = mx4_scale(k.e[2 * h]), hi = mx4_scale(k.e[2 * h + 1]);
+        f1[h] = __byte_perm(lo.f1, hi.f1, 0x5410);
+        f2[h] = __byte_perm(lo.two ? lo.f2 : 0x3F803F80u, hi.two ? hi.f2 : 0x3F803F80u, 0x5410);
+      } else {
+        f1[h] = (k.e[2 * h + 1] * 0x10000u + k.e[2 * h]) * 0x80u + 126u * 0x00800080u;
+      }
     }
 #pragma unroll
     for (int v = 0; v < 2; ++v) {  // nibbles 0..3, 4..7 of the words
@@ -332,8 +394,9 @@ __global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_adjoint(const M
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          mx4_nibbles(__byte_perm(q ? c[2 * h].y : c[2 * h].x, q ? c[2 * h + 1].y : c[2 * h + 1].x, sel), f1[h], w[q][h]);
-          if (two)
+          mx4_nibbles(__byte_perm(q ? k.c[2 * h].y : k.c[2 * h].x, q ? k.c[2 * h + 1].y : k.c[2 * h + 1].x, sel), f1[h],
+                      w[q][h]);
+          if (far.value)
 #pragma unroll
             for (int j = 0; j < 4; ++j) w[q][h][j] = bf16x2_mul(w[q][h][j], f2[h]);
         }
@@ -341,8 +404,35 @@ __global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_adjoint(const M
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int u = 0; u < NT; ++u)
-          mma_16816(acc[4 * v + j][u], w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j], x[u].x, x[u].y);
+          mma_16816(acc[4 * v + j][u], w[0][0][j], w[1][0][j], w[0][1][j], w[1][1][j], k.x[u].x, k.x[u].y);
     }
+  };
+  auto use = [&](const Block& k) {
+    const bool far = max(max(k.e[0], k.e[1]), max(k.e[2], k.e[3])) > 128u;
+    if (__any_sync(0xffffffffu, far)) multiply(k, std::true_type()); else multiply(k, std::false_type());
+  };
+  // AHEAD - 1 blocks are on their way while one is multiplied.
+  constexpr int AHEAD = NT == 1 ? 4 : 2;
+  const int b_full = min(b_hi, a.K / 16);
+  Block ring[AHEAD];
+  int b = b_lo + warp;
+#pragma unroll
+  for (int i = 0; i < AHEAD - 1; ++i)
+    if (b + i * WARPS < b_full) load(ring[i], b + i * WARPS);
+#pragma unroll 1
+  while (b < b_full) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (b + (AHEAD - 1) * WARPS < b_full) load(ring[(i + AHEAD - 1) % AHEAD], b + (AHEAD - 1) * WARPS);
+      if (b < b_full) {
+        use(ring[i]);
+        b += WARPS;
+      }
+    }
+  }
+  if (b < b_hi) {
+    load_end(ring[0], b);
+    use(ring[0]);
   }
   griddep_launch();
   constexpr int F = MX4_FEW_COLS, T = 8 * NT;
@@ -355,7 +445,7 @@ __global__ void __launch_bounds__(MX4_FEW_WARPS * 32, 2) mx4_few_adjoint(const M
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         out[(8 * u + 2 * t + (q & 1)) * F + 16 * g + 8 * (q >> 1) + j] = acc[j][u][q];
-  mx4_few_finish<F, T>(a, red, m0, split);
+  mx4_few_finish<F, T, WARPS>(a, red, m0, split);
 }
 
 // -------------------------------------------------------------------------------- product, many tokens
