@@ -36,23 +36,25 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Eight codes (w: code e in bits 4e..4e+3) to eight bf16 values in column order.  The code's three
+// Eight codes (w: code e in bits 4e..4e+3) to eight bf16 values in column order, times f1.  The code's three
 // magnitude bits, moved to the lowest exponent bits and the highest mantissa bit of a bf16, are the value times
 // 2^-126 (a subnormal for 0 and 1/2), so one exact product with 2^126 times the scale finishes it.  Per pair:
-// one byte permutation puts both codes at the tops of their halves, one shift and two masks place the bits.
-__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, const Mx4Scale& s) {
+// one byte permutation puts both codes at the top of each byte of their halves, a product by 4 (a shift
+// on the multiplier, which has more room than the logic unit) and two masks place the bits.
+__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, uint32_t f1) {
   const uint32_t w4 = w << 4;
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const uint32_t t = __byte_perm(w4, w, ((4 + j) << 12) | ((4 + j) << 8) | (j << 4) | j);
-    o[j] = bf16x2_mul((t & 0x80008000u) | ((t >> 6) & 0x01C001C0u), s.f1);
-  }
-  if (s.two) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = bf16x2_mul(o[j], s.f2);
+    o[j] = bf16x2_mul((t & 0x80008000u) | ((t * 4u) & 0x01C001C0u), f1);
   }
   return make_uint4(o[0], o[1], o[2], o[3]);
+}
+__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, const Mx4Scale& s) {
+  uint4 o = mx4_decode8(w, s.f1);
+  if (s.two) o = make_uint4(bf16x2_mul(o.x, s.f2), bf16x2_mul(o.y, s.f2), bf16x2_mul(o.z, s.f2), bf16x2_mul(o.w, s.f2));
+  return o;
 }
 
 // --------------------------------------------------------------------------- quantisation
@@ -453,16 +455,18 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 // (adjoint), X and Y bf16, sums in fp32.
 //
 // The weight is the 128-row operand (MH of them per CTA: 128 or 256 features), the tokens are the columns (TN of
-// them, a multiple of 16 up to 256), so that few tokens waste nothing of the tile.  One warp streams X tiles and
-// code tiles with TMA into a ring; eight converter warps turn a code tile into a bf16 tile in the
-// 128-byte-swizzled layout of the tensor core (forward: K-major, adjoint: MN-major) in a ring of its own; one
-// thread issues tcgen05.mma; the accumulators (features in TMEM lanes, tokens in columns) go through shared
-// memory as fp32.  Where the tiles alone do not fill the SMs, a cluster of up to 8 CTAs splits K and each CTA
-// sums its share of the tokens over the cluster's shared memory, in a fixed order.
+// them, a multiple of 16 up to 256), so that few tokens waste nothing of the tile.  A k step is 64 positions with 256
+// features and 128 with 128, 16384 weights either way: less work per step and its hand-overs take longer than its
+// products.  One warp streams X tiles and one the codes of MX4_CSTEPS steps at a time (whole 64- or 128-byte
+// rows: with rows of 32 bytes the copies took longer than the products) with TMA into rings; eight converter warps
+// turn a step's codes into a bf16 tile in the 128-byte-swizzled layout of the tensor core (forward: K-major, adjoint:
+// MN-major) in a ring of its own; one thread issues tcgen05.mma; the accumulators have features in TMEM lanes, tokens
+// in columns.  Where the tiles alone do not fill the SMs, a cluster of up to 8 CTAs splits K and each CTA sums its
+// share of the tokens over the cluster's shared memory, in a fixed order.
 struct Mx4Args {
   int M, N, K;           // features out, tokens, features in
   int TN;                // tokens per tile
-  int xs, ws;            // ring depths: X and codes, converted weight
+  int xs, ws, cs;        // ring depths: X, converted weight, codes
   int splits;            // CTAs of a cluster, along K
   const uint8_t* scales;
   long pitch;            // scales per row of the weight
@@ -470,38 +474,45 @@ struct Mx4Args {
 };
 
 constexpr int MX4_CONV = 256;                    // converter threads (warps 0..7)
-constexpr int MX4_THREADS = MX4_CONV + 64;       // + one producer warp, one MMA warp
-constexpr int MX4_BK = 64;
-constexpr int MX4_MAX_RING = 16;
-__host__ __device__ constexpr uint32_t mx4_w_bytes(int mh) { return (uint32_t)mh * 128 * MX4_BK * 2; }
-__host__ __device__ constexpr uint32_t mx4_code_bytes(int mh) { return (uint32_t)mh * 128 * MX4_BK / 2; }
-__host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int xs, int ws) {
-  return (size_t)xs * (tn * MX4_BK * 2 + mx4_code_bytes(mh)) + (size_t)ws * mx4_w_bytes(mh) + 1024 + 512;
+constexpr int MX4_THREADS = MX4_CONV + 96;       // + warps 8 (X), 9 (MMA), 10 (codes)
+constexpr int MX4_CSTEPS = 2;                    // k steps of a code tile
+constexpr int MX4_MAX_RING = 8;
+constexpr uint32_t MX4_W_BYTES = 32768, MX4_C_BYTES = 8192 * MX4_CSTEPS;
+__host__ __device__ constexpr int mx4_bk(int mh) { return 128 / mh; }  // K positions of a step
+// A code tile: bytes of its rows, and its rows.
+__host__ __device__ constexpr int mx4_code_row(int mh, bool adj) { return adj ? 64 * mh : mx4_bk(mh) / 2 * MX4_CSTEPS; }
+__host__ __device__ constexpr int mx4_code_rows(int mh, bool adj) { return adj ? mx4_bk(mh) * MX4_CSTEPS : 128 * mh; }
+__host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int xs, int ws, int cs) {
+  return (size_t)xs * (tn * mx4_bk(mh) * 2) + (size_t)ws * MX4_W_BYTES + (size_t)cs * MX4_C_BYTES + 1024 + 512;
 }
 
 template <int MH, bool ADJ>
 __global__ void __launch_bounds__(MX4_THREADS, 1)
     mx4_gemm_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC, const Mx4Args a) {
   using namespace sm100;
-  constexpr uint32_t W_BYTES = mx4_w_bytes(MH), C_BYTES = mx4_code_bytes(MH);
+  constexpr uint32_t W_BYTES = MX4_W_BYTES, C_BYTES = MX4_C_BYTES;
+  constexpr int CS = MX4_CSTEPS, BK = mx4_bk(MH), KA = BK / 64;  // KA: 64-wide pieces of a step
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t x_bytes = (uint32_t)a.TN * MX4_BK * 2;
+  const uint32_t xa_bytes = (uint32_t)a.TN * 128, x_bytes = xa_bytes * KA;
   uint8_t* wring = smem + (size_t)a.xs * x_bytes;
   uint8_t* cring = wring + (size_t)a.ws * W_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(cring + (size_t)a.xs * C_BYTES);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(cring + (size_t)a.cs * C_BYTES);
   const uint32_t sx = smem_u32(smem), sw = smem_u32(wring), sc = smem_u32(cring), sb = smem_u32(bars);
-  auto full = [&](int s) { return sb + 8u * s; };                            // X and codes have arrived
-  auto empty = [&](int s) { return sb + 8u * (MX4_MAX_RING + s); };          // the products of the stage are done
-  auto conv = [&](int s) { return sb + 8u * (2 * MX4_MAX_RING + s); };       // weight tile converted
-  auto wfree = [&](int s) { return sb + 8u * (2 * MX4_MAX_RING + 4 + s); };  // weight tile consumed
-  const uint32_t accum = sb + 8u * (2 * MX4_MAX_RING + 8);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 2 * MX4_MAX_RING + 9);
+  constexpr uint32_t R = MX4_MAX_RING;
+  auto full = [&](int s) { return sb + 8u * s; };                 // X tile has arrived
+  auto empty = [&](int s) { return sb + 8u * (R + s); };          // its products are done
+  auto conv = [&](int s) { return sb + 8u * (2 * R + s); };       // weight tile converted
+  auto wfree = [&](int s) { return sb + 8u * (3 * R + s); };      // weight tile consumed
+  auto cfull = [&](int s) { return sb + 8u * (4 * R + s); };      // code tile has arrived
+  auto cempty = [&](int s) { return sb + 8u * (5 * R + s); };     // code tile read
+  const uint32_t accum = sb + 8u * (6 * R);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 6 * R + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * (MH * 128);
   const int n0 = blockIdx.y * a.TN;
-  const int KT = (a.K + MX4_BK - 1) / MX4_BK;
+  const int KT = (a.K + BK - 1) / BK;
   const int kt0 = (int)((long)KT * split / a.splits), nkt = (int)((long)KT * (split + 1) / a.splits) - kt0;
   // TMEM columns: MH accumulators of TN, a power of two from 32 up.
   uint32_t cols = 32;
@@ -515,6 +526,10 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     for (int s = 0; s < a.ws; ++s) {
       mbar_init(conv(s), MX4_CONV / 32);
       mbar_init(wfree(s), 1);
+    }
+    for (int s = 0; s < a.cs; ++s) {
+      mbar_init(cfull(s), 1);
+      mbar_init(cempty(s), MX4_CONV / 32);
     }
     mbar_init(accum, 1);
     fence_mbar_init();
@@ -534,176 +549,251 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
 
   if (warp == 8) {
     if (lane == 0) {
-      // ---------------- TMA producer
+      // ---------------- X producer
+      int s = 0;
+      uint32_t phase = 1;
       for (int i = 0; i < nkt; ++i) {
-        const int s = i % a.xs;
-        if (!mbar_wait(empty(s), ((uint32_t)(i / a.xs) & 1u) ^ 1u, KID_MX4, 1)) break;
-        mbar_arrive_expect_tx(full(s), x_bytes + C_BYTES);
-        const int k0 = (kt0 + i) * MX4_BK;
-        if (!ADJ) {
-          tma_load_2d(sc + s * C_BYTES, &tmC, full(s), k0 / 2, m0);  // 32 bytes x 128 MH rows
-        } else {
+        if (!mbar_wait(empty(s), phase, KID_MX4, 1)) break;
+        mbar_arrive_expect_tx(full(s), x_bytes);
 #pragma unroll
-          for (int h = 0; h < 2 * MH; ++h)  // 32 bytes (64 features) x 64 rows each
-            tma_load_2d(sc + s * C_BYTES + h * 2048, &tmC, full(s), m0 / 2 + 32 * h, k0);
-        }
-        tma_load_2d(sx + s * x_bytes, &tmX, full(s), k0, n0);
+        for (int p = 0; p < KA; ++p)
+          tma_load_2d(sx + s * x_bytes + p * xa_bytes, &tmX, full(s), (kt0 + i) * BK + 64 * p, n0);
+        if (++s == a.xs) { s = 0; phase ^= 1u; }
+      }
+    }
+  } else if (warp == 10) {
+    if (lane == 0) {
+      // ---------------- code producer
+      int s = 0;
+      uint32_t phase = 1;
+      for (int i = 0; i < nkt; i += CS) {
+        if (!mbar_wait(cempty(s), phase, KID_MX4, 7)) break;
+        mbar_arrive_expect_tx(cfull(s), C_BYTES);
+        const int k0 = (kt0 + i) * BK;
+        if (!ADJ) tma_load_2d(sc + s * C_BYTES, &tmC, cfull(s), k0 / 2, m0);
+        else tma_load_2d(sc + s * C_BYTES, &tmC, cfull(s), m0 / 2, k0);
+        if (++s == a.cs) { s = 0; phase ^= 1u; }
       }
     }
   } else if (warp == 9) {
     if (lane == 0) {
       // ---------------- MMA issuer
       const uint32_t idesc = idesc_bf16_f32(128, a.TN, ADJ, false);
+      int s = 0, t = 0;
+      uint32_t s_phase = 0, t_phase = 0;
       for (int i = 0; i < nkt; ++i) {
-        const int s = i % a.xs, t = i % a.ws;
-        if (!mbar_wait(full(s), (uint32_t)(i / a.xs) & 1u, KID_MX4, 2)) break;
-        if (!mbar_wait(conv(t), (uint32_t)(i / a.ws) & 1u, KID_MX4, 3)) break;
+        if (!mbar_wait(full(s), s_phase, KID_MX4, 2)) break;
+        if (!mbar_wait(conv(t), t_phase, KID_MX4, 3)) break;
         tc_fence_after();
         const uint32_t xa = sx + s * x_bytes, wa = sw + t * W_BYTES;
+        // The weight tile: MH = 2, 128 features (16 KiB) after the other; MH = 1, forward 64 positions after the
+        // other, adjoint 64 features after the other.
 #pragma unroll
-        for (int kk = 0; kk < MX4_BK / 16; ++kk) {
-          const uint64_t bd = smem_desc_sw128(xa + kk * 32, 16, 1024);
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const uint64_t bd = smem_desc_sw128(xa + (kk >> 2) * xa_bytes + (kk & 3) * 32, 16, 1024);
 #pragma unroll
           for (int h = 0; h < MH; ++h) {
-            const uint64_t ad = ADJ ? smem_desc_sw128(wa + h * 16384 + kk * 2048, 8192, 1024)
-                                    : smem_desc_sw128(wa + h * 16384 + kk * 32, 16, 1024);
+            const uint64_t ad = ADJ ? smem_desc_sw128(wa + h * 16384 + kk * 2048, BK * 128, 1024)
+                                    : smem_desc_sw128(wa + (h + (kk >> 2)) * 16384 + (kk & 3) * 32, 16, 1024);
             mma_bf16(tmem + (uint32_t)(h * a.TN), ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
           }
         }
         mma_commit(empty(s));
         mma_commit(wfree(t));
+        if (++s == a.xs) { s = 0; s_phase ^= 1u; }
+        if (++t == a.ws) { t = 0; t_phase ^= 1u; }
       }
       mma_commit(accum);
     }
   } else {
-    // ---------------- converters: MH blocks of 32 codes per thread and k step
+    // ---------------- converters: two blocks of 32 codes (64 columns) of one row per thread and step
+    // Forward: rows are features, columns K positions.  Adjoint: rows are K positions, columns features.
     const int ct = threadIdx.x;
-    const uint8_t* scale_at[MH];
-    long scale_step;
-    bool live[MH];
-    int src[MH], dst[MH], key;
-    if (!ADJ) {
-      const int row = MH == 1 ? (ct & 127) : ct;
-      key = row & 7;
-      scale_step = MX4_BK / 32;
+    constexpr int ROWS = ADJ ? BK : 128 * MH;
+    const int row = ct & (ROWS - 1), piece = ct / ROWS;  // row of a step's codes, 64 columns of it
+    const int key = row & 7;                             // 128-byte swizzle of the bf16 tile
+    const uint32_t dst = (uint32_t)(piece * ROWS * 128 + row * 128);
+    // Code tile: its 16-byte pieces are swizzled over 128 or 64 bytes.
+    constexpr int CROW = mx4_code_row(MH, ADJ);
+    const uint32_t crow = (uint32_t)(row * CROW);
+    const uint32_t ckey = CROW == 128 ? (uint32_t)(row & 7) : (uint32_t)((row >> 1) & 3);
+    static_assert(CROW == 128 || CROW == 64, "swizzle widths");
+    // Scales of CS steps, two bytes each, loaded a group ahead.  Rows and features past the end repeat the last
+    // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
+    const int nblock = (int)a.pitch, base = ADJ ? m0 / 32 + 2 * piece : 0;
+    const uint8_t* srow = ADJ ? a.scales : a.scales + (long)min(m0 + row, a.M - 1) * a.pitch;
+    // One load for a group (forward) or a step (adjoint) where the rows of scales are aligned for it.
+    const bool wide = ADJ ? a.pitch % 2 == 0 : a.pitch % (BK / 32 * CS) == 0 && kt0 % CS == 0;
+    auto load_scales = [&](int i, uint32_t (&e)[CS]) {
+      if (i >= nkt) return;
+      if (!ADJ) {
+        const int k = (kt0 + i) * (BK / 32);
+        if (wide) {
+          if (KA == 1) {
+            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(srow + k));
+            e[0] = v & 0xFFFFu;
+            e[1] = v >> 16;
+          } else {
+            const uint2 v = __ldg(reinterpret_cast<const uint2*>(srow + k));
+            e[0] = (v.x >> (16 * piece)) & 0xFFFFu;
+            e[1] = (v.y >> (16 * piece)) & 0xFFFFu;
+          }
+        } else {
 #pragma unroll
-      for (int u = 0; u < MH; ++u) {
-        const int b = MH == 1 ? ct >> 7 : u;  // which 32 of the 64 columns
-        src[u] = row * 32 + b * 16;
-        dst[u] = row * 128 + 0 * b;
-        live[u] = m0 + row < a.M;
-        scale_at[u] = a.scales + (long)(m0 + row) * a.pitch + (long)kt0 * scale_step + b;
-      }
-    } else {
-      const int k = ct & 63;
-      key = k & 7;
-      scale_step = MX4_BK * a.pitch;
-#pragma unroll
-      for (int u = 0; u < MH; ++u) {
-        const int b = MH == 1 ? ct >> 6 : (ct >> 6) * 2 + u;  // which 32 of the 128 MH features
-        src[u] = (b >> 1) * 2048 + k * 32 + (b & 1) * 16;
-        dst[u] = (b >> 1) * 8192 + k * 128;
-        live[u] = m0 + 32 * b < a.M;
-        scale_at[u] = a.scales + ((long)kt0 * MX4_BK + k) * a.pitch + m0 / 32 + b;
-      }
-    }
-    // The scale of step i; past the weight's edge, where the codes are zeros, any finite one does.
-    auto load_scale = [&](int i, int u) -> uint32_t {
-      const bool ok = ADJ ? live[u] && (kt0 + i) * MX4_BK + (ct & 63) < a.K
-                          : live[u] && (kt0 + i) * MX4_BK + 32 * (MH == 1 ? ct >> 7 : u) < a.K;
-      return i < nkt && ok ? (uint32_t)__ldg(scale_at[u] + (long)i * scale_step) : 127u;
-    };
-    // Scales are fetched four steps ahead, four steps at a time.
-    uint32_t cur[4][MH], nxt[4][MH];
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int u = 0; u < MH; ++u) nxt[q][u] = load_scale(q, u);
-    bool ok = true;
-    for (int i0 = 0; i0 < nkt && ok; i0 += 4) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int u = 0; u < MH; ++u) {
-          cur[q][u] = nxt[q][u];
-          nxt[q][u] = load_scale(i0 + 4 + q, u);
+          for (int q = 0; q < CS; ++q) {
+            const int c = k + q * (BK / 32) + 2 * piece;
+            e[q] = c < nblock ? (uint32_t)__ldg(srow + c) : 127u;
+            e[q] |= (c + 1 < nblock ? (uint32_t)__ldg(srow + c + 1) : 127u) << 8;
+          }
         }
+      } else {
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int i = i0 + q;
-        if (i < nkt && ok) {
-          const int s = i % a.xs, t = i % a.ws;
-          ok = mbar_wait(full(s), (uint32_t)(i / a.xs) & 1u, KID_MX4, 4);
-          ok = ok && mbar_wait(wfree(t), ((uint32_t)(i / a.ws) & 1u) ^ 1u, KID_MX4, 5);
-          ok = __all_sync(0xffffffffu, ok);
-          if (ok) {
-            const uint8_t* codes = cring + s * C_BYTES;
-            uint8_t* tile = wring + t * W_BYTES;
-#pragma unroll
-            for (int u = 0; u < MH; ++u) {
-              const uint4 c = *reinterpret_cast<const uint4*>(codes + src[u]);
-              const Mx4Scale f = mx4_scale(cur[q][u]);
-              const int half = ADJ ? (MH == 1 ? (ct >> 6) & 1 : u) : (MH == 1 ? ct >> 7 : u);  // 64-byte half of the row
-              const uint32_t w[4] = {c.x, c.y, c.z, c.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                *reinterpret_cast<uint4*>(tile + dst[u] + (((4 * half + j) ^ key) << 4)) = mx4_decode8(w[j], f);
-            }
-            fence_proxy_async_smem();  // the tensor core reads what the threads wrote
-            __syncwarp();
-            if (lane == 0) mbar_arrive(conv(t));
+        for (int q = 0; q < CS; ++q) {
+          const int k = (kt0 + i + q) * BK + row;
+          e[q] = 127u | 127u << 8;
+          if (k < a.K) {
+            const uint8_t* at = srow + (long)k * a.pitch;
+            if (wide) e[q] = __ldg(reinterpret_cast<const uint16_t*>(at + min(base, nblock - 2)));
+            else e[q] = (uint32_t)__ldg(at + min(base, nblock - 1)) | (uint32_t)__ldg(at + min(base + 1, nblock - 1)) << 8;
           }
         }
       }
+    };
+    static_assert(CS == 2, "scales of a group");
+    uint32_t cur[CS] = {}, nxt[CS] = {};
+    load_scales(0, nxt);
+    bool ok = true;
+    int s = 0, t = 0;
+    uint32_t s_phase = 0, t_phase = 1;
+    for (int i0 = 0; i0 < nkt && ok; i0 += CS) {
+#pragma unroll
+      for (int q = 0; q < CS; ++q) cur[q] = nxt[q];
+      load_scales(i0 + CS, nxt);
+      ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
+      const uint8_t* codes = cring + s * C_BYTES + crow;
+#pragma unroll
+      for (int q = 0; q < CS; ++q) {
+        if (i0 + q < nkt) {
+          uint4 c[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t at = (uint32_t)((ADJ ? 0 : 2 * KA * q) + 2 * piece + u);
+            c[u] = *reinterpret_cast<const uint4*>(codes + (ADJ ? q * BK * CROW : 0) + ((at ^ ckey) << 4));
+          }
+          ok = ok && mbar_wait(wfree(t), t_phase, KID_MX4, 5);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+          uint4* tile = reinterpret_cast<uint4*>(wring + t * W_BYTES + dst);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
+            const uint32_t e = (cur[q] >> (8 * u)) & 0xFFu;
+            // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
+            if (__any_sync(0xffffffffu, e > 128u)) {
+              const Mx4Scale f = mx4_scale(e);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) tile[(4 * u + j) ^ key] = mx4_decode8(w[j], f);
+            } else {
+              const uint32_t f1 = e * 0x00800080u + 126u * 0x00800080u;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) tile[(4 * u + j) ^ key] = mx4_decode8(w[j], f1);
+            }
+          }
+          fence_proxy_async_smem();  // the tensor core reads what the threads wrote
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(conv(t));
+            // Only now have all codes of the tile been used: given back right after their loads, before
+            // the wait above, a refill was seen to overtake the loads.  (A last tile cut short is not refilled.)
+            if (q == CS - 1) mbar_arrive(cempty(s));
+          }
+          if (++t == a.ws) { t = 0; t_phase ^= 1u; }
+        }
+      }
+      if (++s == a.cs) { s = 0; s_phase ^= 1u; }
     }
   }
   __syncwarp();
 
-  // ---------------- epilogue, one 128-feature half after the other: fp32 sums through shared memory
+  // ---------------- epilogue
   bool ok = mbar_wait(accum, 0, KID_MX4, 6);
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
   griddep_launch();
-  float* red = reinterpret_cast<float*>(smem);  // [TN][128]: the rings are idle (every load has been consumed)
-  const int share = a.TN / a.splits, c_lo = split * share;
-#pragma unroll 1
-  for (int h = 0; h < MH; ++h) {
+  if (a.splits == 1) {
+    // Warp w drains lanes 32 (w % 4).. of both halves, tokens of the half w / 4: 32 tokens at a time, turned
+    // over in shared memory (the rings are idle: every load has been consumed) so that stores are 16 bytes.
     if (warp < 8 && ok) {
-      // Warp w: lanes 32 (w % 4).., token columns of the half w / 4.
-      const int m = (warp & 3) * 32 + lane, half_n = a.TN / 2;
-      const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN + (warp >> 2) * half_n);
-      float* out = red + (size_t)(warp >> 2) * half_n * 128 + m;
-      for (int c = 0; c < half_n; c += 8) {
-        uint32_t v[8];
-        tmem_ld_32x32b_x8(t0 + (uint32_t)c, v);
-        tmem_wait_ld();
+      const int half_n = a.TN / 2, lq = (warp & 3) * 32, c_lo = (warp >> 2) * half_n;
+      __nv_bfloat16* patch = reinterpret_cast<__nv_bfloat16*>(smem) + warp * 1024;  // [32 tokens][32 features]
+#pragma unroll 1
+      for (int h = 0; h < MH; ++h) {
+        const uint32_t t0 = tmem + ((uint32_t)lq << 16) + (uint32_t)(h * a.TN + c_lo);
+        const int m = m0 + h * 128 + lq + (lane & 3) * 8;
+#pragma unroll 1
+        for (int c = 0; c < half_n; c += 32) {
+          uint32_t v[4][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) out[(size_t)(c + j) * 128] = __uint_as_float(v[j]);
-      }
-    }
-    if (a.splits > 1) cluster_sync_all(); else __syncthreads();
-    if (ok) {
-      // Eight features of one token per step: sum over the cluster, round once, 16-byte store.
-      for (int e = threadIdx.x; e < share * 16; e += MX4_THREADS) {
-        const int c = c_lo + (e >> 4), f = (e & 15) * 8;
-        const int n = n0 + c, m = m0 + h * 128 + f;
-        if (n < a.N && m < a.M) {
-          float x[8] = {};
-          const uint32_t at = smem_u32(red + (size_t)c * 128 + f);
-          for (int r = 0; r < a.splits; ++r) {
-            float y[8];
-            ld_cluster_v4(a.splits > 1 ? mapa_shared(at, (uint32_t)r) : at, y);
-            ld_cluster_v4((a.splits > 1 ? mapa_shared(at, (uint32_t)r) : at) + 16, y + 4);
+          for (int g = 0; g < 4; ++g)
+            if (c + 8 * g < half_n) tmem_ld_32x32b_x8(t0 + (uint32_t)(c + 8 * g), v[g]);
+          tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 8; ++j) x[j] += y[j];
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) patch[(8 * g + j) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[g][j]));
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int n = n0 + c_lo + c + 8 * g + (lane >> 2);
+            if (c + 8 * g < half_n && n < a.N && m < a.M)
+              *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
+                  *reinterpret_cast<const uint4*>(patch + (8 * g + (lane >> 2)) * 32 + (lane & 3) * 8);
           }
-          *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
-              make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          __syncwarp();
         }
       }
     }
-    // The peers have read this CTA's sums before it reuses them or exits.
-    if (a.splits > 1) cluster_sync_all(); else __syncthreads();
+  } else {
+    // One 128-feature half after the other, fp32 sums through shared memory.
+    float* red = reinterpret_cast<float*>(smem);  // [TN][128]
+    const int share = a.TN / a.splits, c_lo = split * share;
+#pragma unroll 1
+    for (int h = 0; h < MH; ++h) {
+      if (warp < 8 && ok) {
+        const int half_n = a.TN / 2;
+        const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN + (warp >> 2) * half_n);
+        float* out = red + (size_t)(warp >> 2) * half_n * 128 + (warp & 3) * 32 + lane;
+        for (int c = 0; c < half_n; c += 8) {
+          uint32_t v[8];
+          tmem_ld_32x32b_x8(t0 + (uint32_t)c, v);
+          tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) out[(size_t)(c + j) * 128] = __uint_as_float(v[j]);
+        }
+      }
+      cluster_sync_all();
+      if (ok) {
+        // Eight features of one token per step: sum over the cluster, round once, 16-byte store.
+        for (int e = threadIdx.x; e < share * 16; e += MX4_THREADS) {
+          const int c = c_lo + (e >> 4), f = (e & 15) * 8;
+          const int n = n0 + c, m = m0 + h * 128 + f;
+          if (n < a.N && m < a.M) {
+            float x[8] = {};
+            const uint32_t at = smem_u32(red + (size_t)c * 128 + f);
+            for (int r = 0; r < a.splits; ++r) {
+              float y[8];
+              ld_cluster_v4(mapa_shared(at, (uint32_t)r), y);
+              ld_cluster_v4(mapa_shared(at, (uint32_t)r) + 16, y + 4);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) x[j] += y[j];
+            }
+            *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
+                make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+          }
+        }
+      }
+      cluster_sync_all();  // the peers have read this CTA's sums before it reuses them or exits
+    }
   }
   tc_fence_before();
   __syncthreads();

@@ -222,8 +222,9 @@ Operand view(const void* base, long rows, long cols, long ld, long zrow = 0, lon
 
 // 2-D tensor map of a row-major bf16 (or fp32) array, 128-byte swizzle; box_inner elements must
 // span 128 bytes (64 bf16 / 32 fp32).  Int8 codes (dt = U8) are mapped unswizzled (the
-// converter warps read them row by row), any box up to 256 x 256.
-bool make_tmap(CUtensorMap* m, const Operand& op, uint32_t box_inner, uint32_t box_outer, int dt = BF16) {
+// converter warps read them row by row) unless told otherwise, any box up to 256 x 256.
+bool make_tmap(CUtensorMap* m, const Operand& op, uint32_t box_inner, uint32_t box_outer, int dt = BF16,
+               CUtensorMapSwizzle u8_swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
   EncodeTiledFn fn = encode_fn();
   if (fn == nullptr) return false;
   const uint64_t es = dt == F32 ? 4 : dt == U8 ? 1 : 2;
@@ -235,7 +236,7 @@ bool make_tmap(CUtensorMap* m, const Operand& op, uint32_t box_inner, uint32_t b
                                    : dt == U8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   return fn(m, type, 2, const_cast<void*>(op.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            dt == U8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            dt == U8 ? u8_swizzle : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
@@ -520,22 +521,30 @@ poetx_status run_w_gemm_q8(const GemmDesc& g, const void* Q, long q_rows, bool q
 
 // ------------------------------------------------------------------------------ MX4 products
 struct Mx4Plan {
-  int mh, tn, xs, ws, splits;
+  int mh, tn, xs, ws, cs, splits;
 };
 Mx4Plan mx4_plan(long M, long N, long K) {
   Mx4Plan p;
-  const long nt = (N + 255) / 256;
-  p.tn = (int)(((N + nt - 1) / nt + 15) / 16 * 16);
+  long nt = (N + 255) / 256;
   // Two halves of 128 features per CTA (the X tile is read once for both) while that still
   // occupies three quarters of the SMs.
-  const long t2 = (M + 255) / 256 * nt, kt = (K + MX4_BK - 1) / MX4_BK;
+  const long t2 = (M + 255) / 256 * nt;
   p.mh = 4 * t2 >= 3L * kNumSms ? 2 : 1;
-  const long tiles = p.mh == 2 ? t2 : (M + 127) / 128 * nt;
+  if (p.mh == 1) nt = (N + 127) / 128;
+  p.tn = (int)(((N + nt - 1) / nt + 15) / 16 * 16);
+  const long tiles = p.mh == 2 ? t2 : (M + 127) / 128 * nt, kt = (K + mx4_bk(p.mh) - 1) / mx4_bk(p.mh);
   p.splits = 1;
-  while (p.splits < 8 && tiles * p.splits * 2 <= kNumSms && kt >= 8L * p.splits) p.splits *= 2;
-  p.ws = p.mh == 2 ? 2 : 3;
+#ifndef KMIN
+#define KMIN 4
+#endif
+  while (p.splits < 8 && tiles * p.splits * 2 <= kNumSms && kt >= (long)KMIN * p.splits) p.splits *= 2;
+#ifdef MX4_TUNE
+  if (const char* v = getenv("MX4P")) sscanf(v, "%d,%d,%d", &p.mh, &p.tn, &p.splits);
+#endif
+  p.ws = 3;
+  p.cs = p.mh == 2 || p.tn > 96 ? 2 : 3;
   p.xs = MX4_MAX_RING;
-  while (p.xs > 4 && mx4_smem_bytes(p.mh, p.tn, p.xs, p.ws) > 227 * 1024) --p.xs;
+  while (p.xs > 2 && mx4_smem_bytes(p.mh, p.tn, p.xs, p.ws, p.cs) > 227 * 1024) --p.xs;
   return p;
 }
 
@@ -552,17 +561,19 @@ poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes
   }
   CUtensorMap tx, tc;
   if (!make_tmap(&tx, X, 64, (uint32_t)p.tn)) return POETX_ERR_CUDA;
-  if (!make_tmap(&tc, codes, 32, ADJ ? 64 : MH * 128, U8)) return POETX_ERR_CUDA;
+  if (!make_tmap(&tc, codes, mx4_code_row(MH, ADJ), mx4_code_rows(MH, ADJ), U8,
+                 mx4_code_row(MH, ADJ) == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B))
+    return POETX_ERR_CUDA;
   Mx4Args a;
   a.M = M; a.N = N; a.K = K;
-  a.TN = p.tn; a.xs = p.xs; a.ws = p.ws; a.splits = p.splits;
+  a.TN = p.tn; a.xs = p.xs; a.ws = p.ws; a.cs = p.cs; a.splits = p.splits;
   a.scales = scales;
   a.pitch = codes.cols / 16;
   a.Y = static_cast<__nv_bfloat16*>(Y);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((M + MH * 128 - 1) / (MH * 128) * p.splits), (unsigned)((N + p.tn - 1) / p.tn), 1);
   cfg.blockDim = dim3(MX4_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = mx4_smem_bytes(MH, p.tn, p.xs, p.ws);
+  cfg.dynamicSmemBytes = mx4_smem_bytes(MH, p.tn, p.xs, p.ws, p.cs);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
