@@ -458,7 +458,7 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 // them, a multiple of 16 up to 256), so that few tokens waste nothing of the tile.  A k step is 64 positions with 256
 // features and 128 with 128, 16384 weights either way: less work per step and its hand-overs take longer than its
 // products.  One warp streams X tiles and one the codes of MX4_CSTEPS steps at a time (whole 64- or 128-byte
-// rows: with rows of 32 bytes the copies took longer than the products) with TMA into rings; eight converter warps
+// rows: with rows of 32 bytes the copies took longer than the products) with TMA into rings; sixteen converter warps
 // turn a step's codes into a bf16 tile in the 128-byte-swizzled layout of the tensor core (forward: K-major, adjoint:
 // MN-major) in a ring of its own; one thread issues tcgen05.mma; the accumulators have features in TMEM lanes, tokens
 // in columns.  Where the tiles alone do not fill the SMs, a cluster of up to 8 CTAs splits K and each CTA sums its
@@ -466,24 +466,26 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 struct Mx4Args {
   int M, N, K;           // features out, tokens, features in
   int TN;                // tokens per tile
-  int xs, ws, cs;        // ring depths: X, converted weight, codes
+  int slots, cs;         // ring depths: tiles of X and converted weight, codes
   int splits;            // CTAs of a cluster, along K
   const uint8_t* scales;
   long pitch;            // scales per row of the weight
   __nv_bfloat16* Y;
 };
 
-constexpr int MX4_CONV = 256;                    // converter threads (warps 0..7)
-constexpr int MX4_THREADS = MX4_CONV + 96;       // + warps 8 (X), 9 (MMA), 10 (codes)
-constexpr int MX4_CSTEPS = 2;                    // k steps of a code tile
+// Two groups of eight converter warps, each with every other step, so that one converts while the other waits for
+// its tiles; then a warp for X (16), for the products (17), for the codes (18).
+constexpr int MX4_GROUP = 256, MX4_CONV_WARPS = 16;
+constexpr int MX4_THREADS = 32 * (MX4_CONV_WARPS + 3);
+constexpr int MX4_CSTEPS = 2;                    // k steps of a code tile, one per group
 constexpr int MX4_MAX_RING = 8;
 constexpr uint32_t MX4_W_BYTES = 32768, MX4_C_BYTES = 8192 * MX4_CSTEPS;
 __host__ __device__ constexpr int mx4_bk(int mh) { return 128 / mh; }  // K positions of a step
 // A code tile: bytes of its rows, and its rows.
 __host__ __device__ constexpr int mx4_code_row(int mh, bool adj) { return adj ? 64 * mh : mx4_bk(mh) / 2 * MX4_CSTEPS; }
 __host__ __device__ constexpr int mx4_code_rows(int mh, bool adj) { return adj ? mx4_bk(mh) * MX4_CSTEPS : 128 * mh; }
-__host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int xs, int ws, int cs) {
-  return (size_t)xs * (tn * mx4_bk(mh) * 2) + (size_t)ws * MX4_W_BYTES + (size_t)cs * MX4_C_BYTES + 1024 + 512;
+__host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int slots, int cs) {
+  return (size_t)slots * (tn * mx4_bk(mh) * 2 + MX4_W_BYTES) + (size_t)cs * MX4_C_BYTES + 1024 + 512;
 }
 
 template <int MH, bool ADJ>
@@ -494,20 +496,17 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   constexpr int CS = MX4_CSTEPS, BK = mx4_bk(MH), KA = BK / 64;  // KA: 64-wide pieces of a step
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const uint32_t xa_bytes = (uint32_t)a.TN * 128, x_bytes = xa_bytes * KA;
-  uint8_t* wring = smem + (size_t)a.xs * x_bytes;
-  uint8_t* cring = wring + (size_t)a.ws * W_BYTES;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(cring + (size_t)a.cs * C_BYTES);
-  const uint32_t sx = smem_u32(smem), sw = smem_u32(wring), sc = smem_u32(cring), sb = smem_u32(bars);
+  // A slot holds a step's converted weight, then its X (64-wide pieces one after the other).
+  const uint32_t xa_bytes = (uint32_t)a.TN * 128, x_bytes = xa_bytes * KA, slot_bytes = W_BYTES + x_bytes;
+  const uint32_t sw = smem_u32(smem), sc = sw + (uint32_t)a.slots * slot_bytes;
+  const uint32_t sb = sc + (uint32_t)a.cs * C_BYTES;
   constexpr uint32_t R = MX4_MAX_RING;
-  auto full = [&](int s) { return sb + 8u * s; };                 // X tile has arrived
-  auto empty = [&](int s) { return sb + 8u * (R + s); };          // its products are done
-  auto conv = [&](int s) { return sb + 8u * (2 * R + s); };       // weight tile converted
-  auto wfree = [&](int s) { return sb + 8u * (3 * R + s); };      // weight tile consumed
-  auto cfull = [&](int s) { return sb + 8u * (4 * R + s); };      // code tile has arrived
-  auto cempty = [&](int s) { return sb + 8u * (5 * R + s); };     // code tile read
-  const uint32_t accum = sb + 8u * (6 * R);
-  uint32_t* holder = reinterpret_cast<uint32_t*>(bars + 6 * R + 1);
+  auto ready = [&](int s) { return sb + 8u * s; };            // X has arrived and the weight is converted
+  auto taken = [&](int s) { return sb + 8u * (R + s); };      // the products are done
+  auto cfull = [&](int s) { return sb + 8u * (2 * R + s); };  // code tile has arrived
+  auto cempty = [&](int s) { return sb + 8u * (3 * R + s); }; // code tile read
+  const uint32_t accum = sb + 8u * (4 * R);
+  uint32_t* holder = reinterpret_cast<uint32_t*>(smem + (sb - sw) + 8 * (4 * R + 1));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * (MH * 128);
@@ -519,17 +518,13 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   while (cols < (uint32_t)(MH * a.TN)) cols <<= 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.xs; ++s) {
-      mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
-    }
-    for (int s = 0; s < a.ws; ++s) {
-      mbar_init(conv(s), MX4_CONV / 32);
-      mbar_init(wfree(s), 1);
+    for (int s = 0; s < a.slots; ++s) {
+      mbar_init(ready(s), MX4_GROUP / 32 + 1);  // the converting group's warps and X's copy
+      mbar_init(taken(s), 1);
     }
     for (int s = 0; s < a.cs; ++s) {
       mbar_init(cfull(s), 1);
-      mbar_init(cempty(s), MX4_CONV / 32);
+      mbar_init(cempty(s), MX4_CONV_WARPS);
     }
     mbar_init(accum, 1);
     fence_mbar_init();
@@ -537,7 +532,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     prefetch_tmap(&tmX);
     prefetch_tmap(&tmC);
   }
-  if (warp == 8) {
+  if (warp == MX4_CONV_WARPS) {
     tmem_alloc(smem_u32(holder), cols);
     tmem_relinquish();
   }
@@ -547,21 +542,21 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   const uint32_t tmem = *holder;
   griddep_wait();  // X, and just after a quantisation the codes, come from earlier launches
 
-  if (warp == 8) {
+  if (warp == MX4_CONV_WARPS) {
     if (lane == 0) {
       // ---------------- X producer
-      int s = 0;
+      int t = 0;
       uint32_t phase = 1;
       for (int i = 0; i < nkt; ++i) {
-        if (!mbar_wait(empty(s), phase, KID_MX4, 1)) break;
-        mbar_arrive_expect_tx(full(s), x_bytes);
+        if (!mbar_wait(taken(t), phase, KID_MX4, 1)) break;
+        mbar_arrive_expect_tx(ready(t), x_bytes);
 #pragma unroll
         for (int p = 0; p < KA; ++p)
-          tma_load_2d(sx + s * x_bytes + p * xa_bytes, &tmX, full(s), (kt0 + i) * BK + 64 * p, n0);
-        if (++s == a.xs) { s = 0; phase ^= 1u; }
+          tma_load_2d(sw + t * slot_bytes + W_BYTES + p * xa_bytes, &tmX, ready(t), (kt0 + i) * BK + 64 * p, n0);
+        if (++t == a.slots) { t = 0; phase ^= 1u; }
       }
     }
-  } else if (warp == 10) {
+  } else if (warp == MX4_CONV_WARPS + 2) {
     if (lane == 0) {
       // ---------------- code producer
       int s = 0;
@@ -575,142 +570,130 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
         if (++s == a.cs) { s = 0; phase ^= 1u; }
       }
     }
-  } else if (warp == 9) {
-    if (lane == 0) {
-      // ---------------- MMA issuer
-      const uint32_t idesc = idesc_bf16_f32(128, a.TN, ADJ, false);
-      int s = 0, t = 0;
-      uint32_t s_phase = 0, t_phase = 0;
-      for (int i = 0; i < nkt; ++i) {
-        if (!mbar_wait(full(s), s_phase, KID_MX4, 2)) break;
-        if (!mbar_wait(conv(t), t_phase, KID_MX4, 3)) break;
-        tc_fence_after();
-        const uint32_t xa = sx + s * x_bytes, wa = sw + t * W_BYTES;
-        // The weight tile: MH = 2, 128 features (16 KiB) after the other; MH = 1, forward 64 positions after the
-        // other, adjoint 64 features after the other.
+  } else if (warp == MX4_CONV_WARPS + 1) {
+    // ---------------- MMA issuer.  Its scheduler also serves converter warps, so that every instruction between two
+    // products costs several cycles: the descriptors' low words are sums with constants, one barrier says that both
+    // operands are there, and one commit frees both.  (With two of each, and whole descriptors built per
+    // product, a step's issue took 1300 cycles, longer than its products: 52.9 us against 44 for 2048 tokens.)
+    const uint32_t idesc = idesc_bf16_f32(128, a.TN, ADJ, false);
+    const bool leader = elect_one();
+    // A weight tile: MH = 2, 128 features (16 KiB) after the other; MH = 1, forward 64 positions after the other,
+    // adjoint 64 features after the other.
+    const uint64_t wd0 = ADJ ? smem_desc_sw128(sw, BK * 128, 1024) : smem_desc_sw128(sw, 16, 1024);
+    const uint64_t xd0 = smem_desc_sw128(sw + W_BYTES, 16, 1024);
+    const uint32_t w_hi = (uint32_t)(wd0 >> 32), x_hi = (uint32_t)(xd0 >> 32);
+    uint32_t w_lo = (uint32_t)wd0, x_lo = (uint32_t)xd0;  // addresses in units of 16 bytes: they never carry
+    int t = 0;
+    uint32_t phase = 0;
+    for (int i = 0; i < nkt; ++i) {
+      if (!__all_sync(0xffffffffu, mbar_wait(ready(t), phase, KID_MX4, 2))) break;
+      tc_fence_after();
+      if (leader) {
 #pragma unroll
         for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint64_t bd = smem_desc_sw128(xa + (kk >> 2) * xa_bytes + (kk & 3) * 32, 16, 1024);
+          const uint32_t xl = x_lo + (kk >= 4 ? xa_bytes >> 4 : 0u) + (kk & 3) * 2;
 #pragma unroll
           for (int h = 0; h < MH; ++h) {
-            const uint64_t ad = ADJ ? smem_desc_sw128(wa + h * 16384 + kk * 2048, BK * 128, 1024)
-                                    : smem_desc_sw128(wa + (h + (kk >> 2)) * 16384 + (kk & 3) * 32, 16, 1024);
-            mma_bf16(tmem + (uint32_t)(h * a.TN), ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+            const uint32_t wl = w_lo + (ADJ ? h * 1024 + kk * 128 : (h + (kk >> 2)) * 1024 + (kk & 3) * 2);
+            mma_bf16_words(tmem + (uint32_t)(h * a.TN), wl, w_hi, xl, x_hi, idesc, kk > 0 || i > 0);
           }
         }
-        mma_commit(empty(s));
-        mma_commit(wfree(t));
-        if (++s == a.xs) { s = 0; s_phase ^= 1u; }
-        if (++t == a.ws) { t = 0; t_phase ^= 1u; }
+        mma_commit(taken(t));
       }
-      mma_commit(accum);
+      __syncwarp();
+      w_lo += slot_bytes >> 4;
+      x_lo += slot_bytes >> 4;
+      if (++t == a.slots) {
+        t = 0;
+        phase ^= 1u;
+        w_lo = (uint32_t)wd0;
+        x_lo = (uint32_t)xd0;
+      }
     }
+    if (leader) mma_commit(accum);
   } else {
     // ---------------- converters: two blocks of 32 codes (64 columns) of one row per thread and step
     // Forward: rows are features, columns K positions.  Adjoint: rows are K positions, columns features.
-    const int ct = threadIdx.x;
+    const int ct = threadIdx.x % MX4_GROUP, group = threadIdx.x / MX4_GROUP;
     constexpr int ROWS = ADJ ? BK : 128 * MH;
     const int row = ct & (ROWS - 1), piece = ct / ROWS;  // row of a step's codes, 64 columns of it
     const int key = row & 7;                             // 128-byte swizzle of the bf16 tile
     const uint32_t dst = (uint32_t)(piece * ROWS * 128 + row * 128);
-    // Code tile: its 16-byte pieces are swizzled over 128 or 64 bytes.
+    // Code tile: its 16-byte pieces are swizzled over 128 or 64 bytes; this group's step of it.
     constexpr int CROW = mx4_code_row(MH, ADJ);
-    const uint32_t crow = (uint32_t)(row * CROW);
-    const uint32_t ckey = CROW == 128 ? (uint32_t)(row & 7) : (uint32_t)((row >> 1) & 3);
     static_assert(CROW == 128 || CROW == 64, "swizzle widths");
-    // Scales of CS steps, two bytes each, loaded a group ahead.  Rows and features past the end repeat the last
+    const uint32_t ckey = CROW == 128 ? (uint32_t)(row & 7) : (uint32_t)((row >> 1) & 3);
+    const uint32_t cpiece = (uint32_t)((ADJ ? 0 : 2 * KA * group) + 2 * piece);
+    const uint32_t c0 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + ((cpiece ^ ckey) << 4);
+    const uint32_t c1 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + (((cpiece + 1) ^ ckey) << 4);
+    // The two scales of a step in 16 bits, loaded eight steps ahead (from HBM that is some 2 us: two steps ahead, their
+    // latency set the pace of small token tiles).  Rows and features past the end repeat the last
     // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
     const int nblock = (int)a.pitch, base = ADJ ? m0 / 32 + 2 * piece : 0;
     const uint8_t* srow = ADJ ? a.scales : a.scales + (long)min(m0 + row, a.M - 1) * a.pitch;
-    // One load for a group (forward) or a step (adjoint) where the rows of scales are aligned for it.
-    const bool wide = ADJ ? a.pitch % 2 == 0 : a.pitch % (BK / 32 * CS) == 0 && kt0 % CS == 0;
-    auto load_scales = [&](int i, uint32_t (&e)[CS]) {
-      if (i >= nkt) return;
+    const bool even = a.pitch % 2 == 0;
+    auto load_scales = [&](int i) -> uint32_t {
+      uint32_t e = 127u | 127u << 8;
       if (!ADJ) {
-        const int k = (kt0 + i) * (BK / 32);
-        if (wide) {
-          if (KA == 1) {
-            const uint32_t v = __ldg(reinterpret_cast<const uint32_t*>(srow + k));
-            e[0] = v & 0xFFFFu;
-            e[1] = v >> 16;
-          } else {
-            const uint2 v = __ldg(reinterpret_cast<const uint2*>(srow + k));
-            e[0] = (v.x >> (16 * piece)) & 0xFFFFu;
-            e[1] = (v.y >> (16 * piece)) & 0xFFFFu;
-          }
-        } else {
-#pragma unroll
-          for (int q = 0; q < CS; ++q) {
-            const int c = k + q * (BK / 32) + 2 * piece;
-            e[q] = c < nblock ? (uint32_t)__ldg(srow + c) : 127u;
-            e[q] |= (c + 1 < nblock ? (uint32_t)__ldg(srow + c + 1) : 127u) << 8;
-          }
+        const int c = (kt0 + i) * (BK / 32) + 2 * piece;
+        if (i < nkt && c < nblock) {
+          if (even) e = __ldg(reinterpret_cast<const uint16_t*>(srow + c));
+          else e = (uint32_t)__ldg(srow + c) | (c + 1 < nblock ? (uint32_t)__ldg(srow + c + 1) : 127u) << 8;
         }
       } else {
-#pragma unroll
-        for (int q = 0; q < CS; ++q) {
-          const int k = (kt0 + i + q) * BK + row;
-          e[q] = 127u | 127u << 8;
-          if (k < a.K) {
-            const uint8_t* at = srow + (long)k * a.pitch;
-            if (wide) e[q] = __ldg(reinterpret_cast<const uint16_t*>(at + min(base, nblock - 2)));
-            else e[q] = (uint32_t)__ldg(at + min(base, nblock - 1)) | (uint32_t)__ldg(at + min(base + 1, nblock - 1)) << 8;
-          }
+        const int k = (kt0 + i) * BK + row;
+        if (i < nkt && k < a.K) {
+          const uint8_t* at = srow + (long)k * a.pitch;
+          if (even) e = __ldg(reinterpret_cast<const uint16_t*>(at + min(base, nblock - 2)));
+          else e = (uint32_t)__ldg(at + min(base, nblock - 1)) | (uint32_t)__ldg(at + min(base + 1, nblock - 1)) << 8;
         }
       }
+      return e;
     };
-    static_assert(CS == 2, "scales of a group");
-    uint32_t cur[CS] = {}, nxt[CS] = {};
-    load_scales(0, nxt);
-    bool ok = true;
-    int s = 0, t = 0;
+    constexpr int AHEAD = 4;
+    uint32_t next[AHEAD];
+#pragma unroll
+    for (int q = 0; q < AHEAD; ++q) next[q] = load_scales(group + CS * q);
+    int s = 0, t = group;  // at least two slots
     uint32_t s_phase = 0, t_phase = 1;
-    for (int i0 = 0; i0 < nkt && ok; i0 += CS) {
+    bool ok = true;
+    for (int i0 = group; i0 < nkt && ok; i0 += CS * AHEAD) {
+#pragma unroll  // so that a scale on its way is never moved between registers, which would wait for it
+      for (int q = 0; q < AHEAD; ++q) {
+        const int i = i0 + CS * q;
+        if (i >= nkt) break;
+        const uint32_t scales = next[q];
+        next[q] = load_scales(i + CS * AHEAD);
+        ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
+        const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
+        ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t tile = sw + t * slot_bytes + dst;
+        const uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
+        // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
+        if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
+          const Mx4Scale f[2] = {mx4_scale(scales & 0xFFu), mx4_scale(scales >> 8)};
 #pragma unroll
-      for (int q = 0; q < CS; ++q) cur[q] = nxt[q];
-      load_scales(i0 + CS, nxt);
-      ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
-      const uint8_t* codes = cring + s * C_BYTES + crow;
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8(w[j], f[j >> 2]));
+        } else {
+          const uint32_t f1[2] = {(scales & 0xFFu) * 0x00800080u + 126u * 0x00800080u,
+                                  (scales >> 8) * 0x00800080u + 126u * 0x00800080u};
 #pragma unroll
-      for (int q = 0; q < CS; ++q) {
-        if (i0 + q < nkt) {
-          uint4 c[2];
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t at = (uint32_t)((ADJ ? 0 : 2 * KA * q) + 2 * piece + u);
-            c[u] = *reinterpret_cast<const uint4*>(codes + (ADJ ? q * BK * CROW : 0) + ((at ^ ckey) << 4));
-          }
-          ok = ok && mbar_wait(wfree(t), t_phase, KID_MX4, 5);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-          uint4* tile = reinterpret_cast<uint4*>(wring + t * W_BYTES + dst);
-#pragma unroll
-          for (int u = 0; u < 2; ++u) {
-            const uint32_t w[4] = {c[u].x, c[u].y, c[u].z, c[u].w};
-            const uint32_t e = (cur[q] >> (8 * u)) & 0xFFu;
-            // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
-            if (__any_sync(0xffffffffu, e > 128u)) {
-              const Mx4Scale f = mx4_scale(e);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) tile[(4 * u + j) ^ key] = mx4_decode8(w[j], f);
-            } else {
-              const uint32_t f1 = e * 0x00800080u + 126u * 0x00800080u;
-#pragma unroll
-              for (int j = 0; j < 4; ++j) tile[(4 * u + j) ^ key] = mx4_decode8(w[j], f1);
-            }
-          }
-          fence_proxy_async_smem();  // the tensor core reads what the threads wrote
-          __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(conv(t));
-            // Only now have all codes of the tile been used: given back right after their loads, before
-            // the wait above, a refill was seen to overtake the loads.  (A last tile cut short is not refilled.)
-            if (q == CS - 1) mbar_arrive(cempty(s));
-          }
-          if (++t == a.ws) { t = 0; t_phase ^= 1u; }
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8(w[j], f1[j >> 2]));
         }
+        fence_proxy_async_smem();  // the tensor core reads what the threads wrote
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(ready(t));
+          // Only now have the codes been used: given back right after their loads, before the wait above, a refill
+          // was seen to overtake the loads.
+          mbar_arrive(cempty(s));
+        }
+        if (++s == a.cs) { s = 0; s_phase ^= 1u; }
+        for (int p = 0; p < CS; ++p)
+          if (++t == a.slots) { t = 0; t_phase ^= 1u; }
       }
-      if (++s == a.cs) { s = 0; s_phase ^= 1u; }
     }
   }
   __syncwarp();
@@ -721,33 +704,33 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   tc_fence_after();
   griddep_launch();
   if (a.splits == 1) {
-    // Warp w drains lanes 32 (w % 4).. of both halves, tokens of the half w / 4: 32 tokens at a time, turned
+    // Warp w drains lanes 32 (w % 4).. of the accumulators, tokens 32 (w / 4).. of every 128: 32 at a time, turned
     // over in shared memory (the rings are idle: every load has been consumed) so that stores are 16 bytes.
-    if (warp < 8 && ok) {
-      const int half_n = a.TN / 2, lq = (warp & 3) * 32, c_lo = (warp >> 2) * half_n;
-      __nv_bfloat16* patch = reinterpret_cast<__nv_bfloat16*>(smem) + warp * 1024;  // [32 tokens][32 features]
+    if (warp < MX4_CONV_WARPS && ok) {
+      const int lq = (warp & 3) * 32;
+      const uint32_t patch = sw + warp * 2048;  // bf16 [32 tokens][32 features]
 #pragma unroll 1
       for (int h = 0; h < MH; ++h) {
-        const uint32_t t0 = tmem + ((uint32_t)lq << 16) + (uint32_t)(h * a.TN + c_lo);
+        const uint32_t t0 = tmem + ((uint32_t)lq << 16) + (uint32_t)(h * a.TN);
         const int m = m0 + h * 128 + lq + (lane & 3) * 8;
 #pragma unroll 1
-        for (int c = 0; c < half_n; c += 32) {
+        for (int c = (warp >> 2) * 32; c < a.TN; c += 128) {
           uint32_t v[4][8];
 #pragma unroll
           for (int g = 0; g < 4; ++g)
-            if (c + 8 * g < half_n) tmem_ld_32x32b_x8(t0 + (uint32_t)(c + 8 * g), v[g]);
+            if (c + 8 * g < a.TN) tmem_ld_32x32b_x8(t0 + (uint32_t)(c + 8 * g), v[g]);
           tmem_wait_ld();
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) patch[(8 * g + j) * 32 + lane] = __float2bfloat16_rn(__uint_as_float(v[g][j]));
+            for (int j = 0; j < 8; ++j) st_shared_b16(patch + ((8 * g + j) * 32 + lane) * 2, __float2bfloat16_rn(__uint_as_float(v[g][j])));
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
-            const int n = n0 + c_lo + c + 8 * g + (lane >> 2);
-            if (c + 8 * g < half_n && n < a.N && m < a.M)
+            const int n = n0 + c + 8 * g + (lane >> 2);
+            if (c + 8 * g < a.TN && n < a.N && m < a.M)
               *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
-                  *reinterpret_cast<const uint4*>(patch + (8 * g + (lane >> 2)) * 32 + (lane & 3) * 8);
+                  ld_shared_v4(patch + (8 * g + (lane >> 2)) * 64 + (lane & 3) * 16);
           }
           __syncwarp();
         }
@@ -755,20 +738,19 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     }
   } else {
     // One 128-feature half after the other, fp32 sums through shared memory.
-    float* red = reinterpret_cast<float*>(smem);  // [TN][128]
+    // red: fp32 [TN][128] at the start of the rings
     const int share = a.TN / a.splits, c_lo = split * share;
 #pragma unroll 1
     for (int h = 0; h < MH; ++h) {
-      if (warp < 8 && ok) {
-        const int half_n = a.TN / 2;
-        const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN + (warp >> 2) * half_n);
-        float* out = red + (size_t)(warp >> 2) * half_n * 128 + (warp & 3) * 32 + lane;
-        for (int c = 0; c < half_n; c += 8) {
+      if (warp < MX4_CONV_WARPS && ok) {
+        const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN);
+        const uint32_t out = sw + ((warp & 3) * 32 + lane) * 4;
+        for (int c = (warp >> 2) * 8; c < a.TN; c += 32) {
           uint32_t v[8];
           tmem_ld_32x32b_x8(t0 + (uint32_t)c, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 8; ++j) out[(size_t)(c + j) * 128] = __uint_as_float(v[j]);
+          for (int j = 0; j < 8; ++j) st_shared_b32(out + (uint32_t)(c + j) * 512, v[j]);
         }
       }
       cluster_sync_all();
@@ -779,7 +761,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
           const int n = n0 + c, m = m0 + h * 128 + f;
           if (n < a.N && m < a.M) {
             float x[8] = {};
-            const uint32_t at = smem_u32(red + (size_t)c * 128 + f);
+            const uint32_t at = sw + (uint32_t)(c * 128 + f) * 4;
             for (int r = 0; r < a.splits; ++r) {
               float y[8];
               ld_cluster_v4(mapa_shared(at, (uint32_t)r), y);
@@ -797,7 +779,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) tmem_dealloc(tmem, cols);
+  if (warp == MX4_CONV_WARPS) tmem_dealloc(tmem, cols);
 }
 
 }  // namespace poetx

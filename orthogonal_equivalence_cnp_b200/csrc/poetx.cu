@@ -521,7 +521,7 @@ poetx_status run_w_gemm_q8(const GemmDesc& g, const void* Q, long q_rows, bool q
 
 // ------------------------------------------------------------------------------ MX4 products
 struct Mx4Plan {
-  int mh, tn, xs, ws, cs, splits;
+  int mh, tn, slots, cs, splits;
 };
 Mx4Plan mx4_plan(long M, long N, long K) {
   Mx4Plan p;
@@ -541,10 +541,15 @@ Mx4Plan mx4_plan(long M, long N, long K) {
 #ifdef MX4_TUNE
   if (const char* v = getenv("MX4P")) sscanf(v, "%d,%d,%d", &p.mh, &p.tn, &p.splits);
 #endif
-  p.ws = 3;
-  p.cs = p.mh == 2 || p.tn > 96 ? 2 : 3;
-  p.xs = MX4_MAX_RING;
-  while (p.xs > 2 && mx4_smem_bytes(p.mh, p.tn, p.xs, p.ws, p.cs) > 227 * 1024) --p.xs;
+  // Shared memory: four slots for the products where they fit, then code tiles, then more slots.
+  auto slots_for = [&](int cs) {
+    int n = MX4_MAX_RING;
+    while (n > 2 && mx4_smem_bytes(p.mh, p.tn, n, cs) > 227 * 1024) --n;
+    return n;
+  };
+  p.cs = 2;
+  while (p.cs < 4 && slots_for(p.cs + 1) >= std::min(4, slots_for(2))) ++p.cs;
+  p.slots = slots_for(p.cs);
   return p;
 }
 
@@ -566,14 +571,14 @@ poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes
     return POETX_ERR_CUDA;
   Mx4Args a;
   a.M = M; a.N = N; a.K = K;
-  a.TN = p.tn; a.xs = p.xs; a.ws = p.ws; a.cs = p.cs; a.splits = p.splits;
+  a.TN = p.tn; a.slots = p.slots; a.cs = p.cs; a.splits = p.splits;
   a.scales = scales;
   a.pitch = codes.cols / 16;
   a.Y = static_cast<__nv_bfloat16*>(Y);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)((M + MH * 128 - 1) / (MH * 128) * p.splits), (unsigned)((N + p.tn - 1) / p.tn), 1);
   cfg.blockDim = dim3(MX4_THREADS, 1, 1);
-  cfg.dynamicSmemBytes = mx4_smem_bytes(MH, p.tn, p.xs, p.ws, p.cs);
+  cfg.dynamicSmemBytes = mx4_smem_bytes(MH, p.tn, p.slots, p.cs);
   cfg.stream = st;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
