@@ -36,23 +36,31 @@ __device__ __forceinline__ uint32_t bf16x2_mul(uint32_t a, uint32_t b) {
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
-// Eight codes (w: code e in bits 4e..4e+3) to eight bf16 values in column order, times f1.  The code's three
-// magnitude bits, moved to the lowest exponent bits and the highest mantissa bit of a bf16, are the value times
-// 2^-126 (a subnormal for 0 and 1/2), so one exact product with 2^126 times the scale finishes it.  Per pair:
-// one byte permutation puts both codes at the top of each byte of their halves, a product by 4 (a shift
-// on the multiplier, which has more room than the logic unit) and two masks place the bits.
-__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, uint32_t f1) {
-  const uint32_t w4 = w << 4;
-  uint32_t o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t t = __byte_perm(w4, w, ((4 + j) << 12) | ((4 + j) << 8) | (j << 4) | j);
-    o[j] = bf16x2_mul((t & 0x80008000u) | ((t * 4u) & 0x01C001C0u), f1);
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
+// A word of four nibbles in each half (bits 4i..4i+3) to four bf16x2: result i holds nibble i of both
+// halves, times f1.  Masked, a nibble s e e m times 2^6 + 2^12 puts e e m at a bf16's lowest exponent and
+// highest mantissa bits and s at its sign: the value times 2^-126 (a subnormal for 0 and 1/2), so one exact
+// product with 2^126 times the scale finishes it.  Integer logic runs at half the rate of multiplications here and
+// is what bounds decoding, hence the multiplication in place of two shifts: 9 logic operations for eight weights.
+__device__ __forceinline__ void mx4_nibbles(uint32_t p, uint32_t f1, uint32_t (&o)[4]) {
+  const uint32_t q = p >> 8;
+  o[0] = bf16x2_mul(((p & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
+  o[1] = bf16x2_mul(((p & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
+  o[2] = bf16x2_mul(((q & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
+  o[3] = bf16x2_mul(((q & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
 }
+// Eight codes (w: code e in bits 4e..4e+3) to eight bf16 values, times f1: in column order (four permutations
+// more), or in the order 0, 4, 1, 5, 2, 6, 3, 7 as mx4_nibbles has them.
+template <bool ORDERED = true>
+__device__ __forceinline__ uint4 mx4_decode8(uint32_t w, uint32_t f1) {
+  uint32_t o[4];
+  mx4_nibbles(w, f1, o);
+  if (!ORDERED) return make_uint4(o[0], o[1], o[2], o[3]);
+  return make_uint4(__byte_perm(o[0], o[1], 0x5410), __byte_perm(o[2], o[3], 0x5410), __byte_perm(o[0], o[1], 0x7632),
+                    __byte_perm(o[2], o[3], 0x7632));
+}
+template <bool ORDERED = true>
 __device__ __forceinline__ uint4 mx4_decode8(uint32_t w, const Mx4Scale& s) {
-  uint4 o = mx4_decode8(w, s.f1);
+  uint4 o = mx4_decode8<ORDERED>(w, s.f1);
   if (s.two) o = make_uint4(bf16x2_mul(o.x, s.f2), bf16x2_mul(o.y, s.f2), bf16x2_mul(o.z, s.f2), bf16x2_mul(o.w, s.f2));
   return o;
 }
@@ -115,18 +123,6 @@ __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __r
 }
 
 // ------------------------------------------------------------------- product, few tokens
-// A word of four nibbles in each half (bits 4i..4i+3) to four bf16x2: result i holds nibble i of both
-// halves, times f1.  Masked, a nibble s e e m times 2^6 + 2^12 puts e e m at a bf16's lowest exponent and
-// highest mantissa bits and s at its sign.  Integer logic runs at half the rate of multiplications here and
-// is what bounds the kernels below, hence the multiplication in place of two shifts: 9 logic operations for
-// eight weights (mx4_decode8, which keeps the columns' order, takes 17).
-__device__ __forceinline__ void mx4_nibbles(uint32_t p, uint32_t f1, uint32_t (&o)[4]) {
-  const uint32_t q = p >> 8;
-  o[0] = bf16x2_mul(((p & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
-  o[1] = bf16x2_mul(((p & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
-  o[2] = bf16x2_mul(((q & 0x000F000Fu) * 0x1040u) & 0x81C081C0u, f1);
-  o[3] = bf16x2_mul(((q & 0x00F000F0u) * 0x0104u) & 0x81C081C0u, f1);
-}
 __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                           uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -675,12 +671,12 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
         if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
           const Mx4Scale f[2] = {mx4_scale(scales & 0xFFu), mx4_scale(scales >> 8)};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8(w[j], f[j >> 2]));
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8<!ADJ>(w[j], f[j >> 2]));
         } else {
           const uint32_t f1[2] = {(scales & 0xFFu) * 0x00800080u + 126u * 0x00800080u,
                                   (scales >> 8) * 0x00800080u + 126u * 0x00800080u};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8(w[j], f1[j >> 2]));
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8<!ADJ>(w[j], f1[j >> 2]));
         }
         fence_proxy_async_smem();  // the tensor core reads what the threads wrote
         __syncwarp();
@@ -703,6 +699,8 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
   griddep_launch();
+  // The adjoint's features stand in mx4_decode8's order within each eight: this lane's.
+  const int feature = ADJ ? (lane & 24) | ((lane >> 1) & 3) | ((lane & 1) << 2) : lane;
   if (a.splits == 1) {
     // Warp w drains lanes 32 (w % 4).. of the accumulators, tokens 32 (w / 4).. of every 128: 32 at a time, turned
     // over in shared memory (the rings are idle: every load has been consumed) so that stores are 16 bytes.
@@ -723,7 +721,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) st_shared_b16(patch + ((8 * g + j) * 32 + lane) * 2, __float2bfloat16_rn(__uint_as_float(v[g][j])));
+            for (int j = 0; j < 8; ++j) st_shared_b16(patch + ((8 * g + j) * 32 + feature) * 2, __float2bfloat16_rn(__uint_as_float(v[g][j])));
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -744,7 +742,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     for (int h = 0; h < MH; ++h) {
       if (warp < MX4_CONV_WARPS && ok) {
         const uint32_t t0 = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (uint32_t)(h * a.TN);
-        const uint32_t out = sw + ((warp & 3) * 32 + lane) * 4;
+        const uint32_t out = sw + ((warp & 3) * 32 + feature) * 4;
         for (int c = (warp >> 2) * 8; c < a.TN; c += 32) {
           uint32_t v[8];
           tmem_ld_32x32b_x8(t0 + (uint32_t)c, v);
