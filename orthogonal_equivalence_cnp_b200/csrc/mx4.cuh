@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 // share of the tokens over the cluster's shared memory, in a fixed order.
 struct Mx4Args {
   int M, N, K;           // features out, tokens, features in
-  int TN;                // tokens per tile
+  int TN, mt;            // tokens per tile; tiles along the features
   int slots, cs;         // ring depths: tiles of X and converted weight, codes
   int splits;            // CTAs of a cluster, along K
   const uint8_t* scales;
@@ -505,8 +505,10 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + (sb - sw) + 8 * (4 * R + 1));
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * (MH * 128);
-  const int n0 = blockIdx.y * a.TN;
+  // Blocks that run together share X tiles and read the whole weight between them.
+  const uint32_t tile_id = blockIdx.x / (uint32_t)a.splits;
+  const int split = (int)(blockIdx.x % (uint32_t)a.splits), m0 = (int)(tile_id % (uint32_t)a.mt) * (MH * 128);
+  const int n0 = (int)(tile_id / (uint32_t)a.mt) * a.TN;
   const int KT = (a.K + BK - 1) / BK;
   const int kt0 = (int)((long)KT * split / a.splits), nkt = (int)((long)KT * (split + 1) / a.splits) - kt0;
   // TMEM columns: MH accumulators of TN, a power of two from 32 up.
