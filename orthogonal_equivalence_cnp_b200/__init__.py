@@ -216,11 +216,11 @@ def _nbytes(x):
     return x.numel() * x.element_size()
 
 
-def _stream(s):
+def _stream(s, device=None):
     if s is None:
         # The raw handle of the current stream: building torch's Stream object for it costs 3 us, more than a launch.
-        torch = _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        torch = _torch_module or _torch()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -395,6 +395,8 @@ def _array(x, name, numel, dtypes, device):
     `dtypes` and lie on the current device, where the library launches."""
     if x is None or isinstance(x, int):
         return x
+    if x.dtype in dtypes and x.numel() >= numel and x.get_device() == device and x.is_contiguous():
+        return x.data_ptr()
     if x.dtype not in dtypes:
         raise ValueError(f"{name}: expected {' or '.join(map(str, dtypes))}, got {x.dtype}")
     if x.numel() < numel:
@@ -403,46 +405,63 @@ def _array(x, name, numel, dtypes, device):
         raise ValueError(f"{name}: array arguments must be CUDA tensors (or raw device addresses)")
     if not x.is_contiguous():
         raise ValueError(f"{name}: array arguments must be contiguous")
-    if x.get_device() != device:
-        raise ValueError(f"{name} is on cuda:{x.get_device()}, not on the current device cuda:{device}")
-    return x.data_ptr()
+    raise ValueError(f"{name} is on cuda:{x.get_device()}, not on the current device cuda:{device}")
 
 
 _mx4_types = None
 
 
-def _mx4(rows, cols, codes, scales, *others):
-    """Addresses of codes, scales and others (x, name, numel, POETX_ dtype) for one MX4 call.  Codes of two
-    weights a byte and E8M0 scales are uint8, or of torch's own types for them."""
+def _mx4_setup():
+    """Types of codes and scales (two weights a byte and E8M0, as uint8 or under torch's own names) and of values,
+    and the current device."""
     global _mx4_types
     torch = _torch()
     if _mx4_types is None:
         _mx4_types = ((torch.uint8, torch.float4_e2m1fn_x2), (torch.uint8, torch.float8_e8m0fnu),
-                      {POETX_BF16: (torch.bfloat16,), POETX_F32: (torch.float32,)})
-    code_types, scale_types, types = _mx4_types
-    dev = torch.cuda.current_device() if torch.cuda.is_initialized() else 0
-    out = [_array(codes, "codes", rows * cols // 2, code_types, dev),
-           _array(scales, "scales", rows * cols // POETX_MX4_BLOCK, scale_types, dev)]
-    for x, name, numel, dtype in others:
-        out.append(_array(x, name, numel, types[dtype], dev))
-    return out
+                      (torch.bfloat16,), (torch.float32,))
+    return (*_mx4_types, torch.cuda.current_device() if torch.cuda.is_initialized() else 0)
+
+
+def _mx4(rows, cols, codes, scales):
+    """Addresses of the codes and scales of a weight."""
+    ct, st, _, _, dev = _mx4_setup()
+    return (_array(codes, "codes", rows * cols // 2, ct, dev),
+            _array(scales, "scales", rows * cols // POETX_MX4_BLOCK, st, dev))
 
 
 def poetx_mx4_quantize(dtype, rows, cols, W, codes, scales, stream=None):
-    c, s, w = _mx4(rows, cols, codes, scales, (W, "W", rows * cols, POETX_BF16 if dtype == POETX_BF16 else POETX_F32))
-    _check(lib().poetx_mx4_quantize(dtype, rows, cols, w, c, s, _stream(stream)), "poetx_mx4_quantize")
+    ct, st, bf, f32, dev = _mx4_setup()
+    n = rows * cols
+    w = _array(W, "W", n, bf if dtype == POETX_BF16 else f32, dev)
+    c = _array(codes, "codes", n // 2, ct, dev)
+    s = _array(scales, "scales", n // POETX_MX4_BLOCK, st, dev)
+    status = (_lib or lib()).poetx_mx4_quantize(dtype, rows, cols, w, c, s, _stream(stream, dev))
+    if status:
+        _check(status, "poetx_mx4_quantize")
 
 
 def poetx_mx4_dequantize(rows, cols, codes, scales, W, stream=None):
-    c, s, w = _mx4(rows, cols, codes, scales, (W, "W", rows * cols, POETX_BF16))
-    _check(lib().poetx_mx4_dequantize(rows, cols, c, s, w, _stream(stream)), "poetx_mx4_dequantize")
+    ct, st, bf, _, dev = _mx4_setup()
+    n = rows * cols
+    c = _array(codes, "codes", n // 2, ct, dev)
+    s = _array(scales, "scales", n // POETX_MX4_BLOCK, st, dev)
+    w = _array(W, "W", n, bf, dev)
+    status = (_lib or lib()).poetx_mx4_dequantize(rows, cols, c, s, w, _stream(stream, dev))
+    if status:
+        _check(status, "poetx_mx4_dequantize")
 
 
 def poetx_mx4_matmul(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, stream=None):
-    c, s, x, y = _mx4(d_out, d_in, codes, scales, (X, "X", n_tokens * (d_out if adjoint else d_in), POETX_BF16),
-                      (Y, "Y", n_tokens * (d_in if adjoint else d_out), POETX_BF16))
-    _check(lib().poetx_mx4_matmul(1 if adjoint else 0, n_tokens, d_in, d_out, x, c, s, y, _stream(stream)),
-           "poetx_mx4_matmul")
+    ct, st, bf, _, dev = _mx4_setup()
+    n = d_out * d_in
+    x = _array(X, "X", n_tokens * (d_out if adjoint else d_in), bf, dev)
+    c = _array(codes, "codes", n // 2, ct, dev)
+    s = _array(scales, "scales", n // POETX_MX4_BLOCK, st, dev)
+    y = _array(Y, "Y", n_tokens * (d_in if adjoint else d_out), bf, dev)
+    status = (_lib or lib()).poetx_mx4_matmul(1 if adjoint else 0, n_tokens, d_in, d_out, x, c, s, y,
+                                              _stream(stream, dev))
+    if status:
+        _check(status, "poetx_mx4_matmul")
 
 
 def poetx_mx4_forward(desc, n_tokens, X, codes, scales, perm_L, perm_R, Q_R, Q_P, Y, workspace, ws_bytes=None,
