@@ -68,58 +68,87 @@ __device__ __forceinline__ uint4 mx4_decode8(uint32_t w, const Mx4Scale& s) {
 // --------------------------------------------------------------------------- quantisation
 // A thread takes eight columns, four threads one scale: the block's largest magnitude meets by two
 // shuffles, its exponent gives the scale, and the values times the scale's inverse (a power of two: exact)
-// round to nearest even in the conversion instruction.  One pass, coalesced both ways: HBM bound.
+// round to nearest even in the conversion instruction.  One pass, coalesced both ways: HBM bound, so each thread
+// has MX4_AT_ONCE pieces' loads under way before it works on the first.
+constexpr int MX4_AT_ONCE = 4;
 template <bool BF>
-__global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* __restrict__ W, long chunks,
+__device__ __forceinline__ void mx4_quantize8(const uint4 (&in)[2], long i, uint32_t mask, uint32_t* codes, uint8_t* scales) {
+  float x[8];
+  const uint32_t w0[4] = {in[0].x, in[0].y, in[0].z, in[0].w}, w1[4] = {in[1].x, in[1].y, in[1].z, in[1].w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    if (BF) {
+      x[2 * e] = __uint_as_float(w0[e] << 16);
+      x[2 * e + 1] = __uint_as_float(w0[e] & 0xFFFF0000u);
+    } else {
+      x[e] = __uint_as_float(w0[e]);
+      x[4 + e] = __uint_as_float(w1[e]);
+    }
+  }
+  uint32_t top = 0u;  // magnitudes ordered as integers: infinities and NaN end on top
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(x[e])));
+  top = max(top, __shfl_xor_sync(mask, top, 1));
+  top = max(top, __shfl_xor_sync(mask, top, 2));
+  uint32_t w = 0u, scale = 255u;  // a block with a NaN or an infinity reads back as NaN
+  if (top < 0x7F800000u) {
+    scale = (uint32_t)max((int)(top >> 23) - 2, 0);
+    const float inv = __uint_as_float((254u - scale) << 23);  // 2^(127 - scale); scale <= 252, so a normal number
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_E2M1,
+                                              cudaRoundNearest)
+           << (8 * e);
+  }
+  codes[i] = w;
+  if ((i & 3) == 0) scales[i >> 2] = (uint8_t)scale;
+}
+
+template <bool BF>
+__global__ void __launch_bounds__(256) mx4_quantize_kernel(const uint4* __restrict__ W, long chunks,
                                                            uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   sm100::griddep_wait();
+  constexpr int U = BF ? MX4_AT_ONCE : MX4_AT_ONCE / 2, V = BF ? 1 : 2;  // 16-byte loads per chunk: V
+  // Chunks and strides are multiples of 4: the shuffles' partners are all here or none is.
   const long stride = (long)gridDim.x * blockDim.x;
-  // chunks is a multiple of 4, and so is every thread's group: the shuffles' partners are all here or none is.
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < chunks; i += stride) {
+  long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (; i + (U - 1) * stride < chunks; i += U * stride) {
     const uint32_t mask = __activemask();
-    float x[8];
-    if (BF) {
-      const uint4 u = reinterpret_cast<const uint4*>(W)[i];
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint4 in[U][2] = {};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    } else {
-      const float4 a = reinterpret_cast<const float4*>(W)[2 * i], b = reinterpret_cast<const float4*>(W)[2 * i + 1];
-      x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-      x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-    }
-    uint32_t top = 0u;  // magnitudes ordered as integers: infinities and NaN end on top
+    for (int u = 0; u < U; ++u)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(fabsf(x[e])));
-    top = max(top, __shfl_xor_sync(mask, top, 1));
-    top = max(top, __shfl_xor_sync(mask, top, 2));
-    uint32_t w = 0u, scale = 255u;  // a block with a NaN or an infinity reads back as NaN
-    if (top < 0x7F800000u) {
-      scale = (uint32_t)max((int)(top >> 23) - 2, 0);
-      // 2^(127 - scale); scale <= 252, and 2^-126 is the smallest normal number.
-      const float inv = scale <= 253u ? __uint_as_float((254u - scale) << 23) : 0.f;
+      for (int v = 0; v < V; ++v) in[u][v] = W[(i + u * stride) * V + v];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * e] * inv, x[2 * e + 1] * inv), __NV_E2M1,
-                                                cudaRoundNearest)
-             << (8 * e);
-    }
-    codes[i] = w;
-    if ((i & 3) == 0) scales[i >> 2] = (uint8_t)scale;
+    for (int u = 0; u < U; ++u) mx4_quantize8<BF>(in[u], i + u * stride, mask, codes, scales);
+  }
+  for (; i < chunks; i += stride) {
+    const uint32_t mask = __activemask();
+    uint4 in[2] = {};
+#pragma unroll
+    for (int v = 0; v < V; ++v) in[v] = W[i * V + v];
+    mx4_quantize8<BF>(in, i, mask, codes, scales);
   }
 }
 
-// bf16 values of codes and scales, eight columns per thread step.
+// bf16 values of codes and scales, eight columns per piece.
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint32_t* __restrict__ codes,
                                                              const uint8_t* __restrict__ scales, long chunks,
                                                              uint4* __restrict__ W) {
   sm100::griddep_wait();
   const long stride = (long)gridDim.x * blockDim.x;
-  for (long i = (long)blockIdx.x * blockDim.x + threadIdx.x; i < chunks; i += stride)
-    W[i] = mx4_decode8(codes[i], mx4_scale(scales[i >> 2]));
+  long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
+  for (; i + (MX4_AT_ONCE - 1) * stride < chunks; i += MX4_AT_ONCE * stride) {
+    uint32_t w[MX4_AT_ONCE], e[MX4_AT_ONCE];
+#pragma unroll
+    for (int u = 0; u < MX4_AT_ONCE; ++u) {
+      w[u] = codes[i + u * stride];
+      e[u] = scales[(i + u * stride) >> 2];
+    }
+#pragma unroll
+    for (int u = 0; u < MX4_AT_ONCE; ++u) W[i + u * stride] = mx4_decode8(w[u], mx4_scale(e[u]));
+  }
+  for (; i < chunks; i += stride) W[i] = mx4_decode8(codes[i], mx4_scale(scales[i >> 2]));
 }
 
 // ------------------------------------------------------------------- product, few tokens

@@ -2095,12 +2095,19 @@ static poetx_status check_mx4_layer(const poetx_desc* desc) {
   return check_mx4(desc->d_in, desc->d_out);
 }
 
+// One batch of pieces per thread (14336 x 4096 from bf16: quantise 24.6 us and read back 25.3, against 27.5 and 27.5
+// with 16 blocks per SM looping over single pieces; 22.7 is the floor of both).
+static int mx4_grid(long chunks) {
+  constexpr long per_block = 256 * MX4_AT_ONCE;
+  return (int)std::min<long>((chunks + per_block - 1) / per_block, 1L << 24);
+}
+
 static poetx_status mx4_quantize(poetx_dtype dtype, long rows, long cols, const void* W, uint8_t* codes,
                                  uint8_t* scales, cudaStream_t st) {
   const long chunks = rows * cols / 8;
   LaunchScope ls(POETX_KC_ELEMENTWISE, st);
-  if (launch_pdl(dtype == POETX_BF16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>, dim3(ew_grid(chunks)),
-                 dim3(256), 0, st, W, chunks, reinterpret_cast<uint32_t*>(codes), scales) != cudaSuccess)
+  if (launch_pdl(dtype == POETX_BF16 ? mx4_quantize_kernel<true> : mx4_quantize_kernel<false>, dim3(mx4_grid(chunks)),
+                 dim3(256), 0, st, static_cast<const uint4*>(W), chunks, reinterpret_cast<uint32_t*>(codes), scales) != cudaSuccess)
     return POETX_ERR_CUDA;
   return last_launch();
 }
@@ -2109,7 +2116,7 @@ static poetx_status mx4_dequantize(long rows, long cols, const uint8_t* codes, c
                                    cudaStream_t st) {
   const long chunks = rows * cols / 8;
   LaunchScope ls(POETX_KC_ELEMENTWISE, st);
-  if (launch_pdl(mx4_dequantize_kernel, dim3(ew_grid(chunks)), dim3(256), 0, st,
+  if (launch_pdl(mx4_dequantize_kernel, dim3(mx4_grid(chunks)), dim3(256), 0, st,
                  reinterpret_cast<const uint32_t*>(codes), scales, chunks, static_cast<uint4*>(W)) != cudaSuccess)
     return POETX_ERR_CUDA;
   return last_launch();
