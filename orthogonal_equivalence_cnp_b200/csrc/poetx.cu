@@ -2096,9 +2096,10 @@ static poetx_status check_mx4_layer(const poetx_desc* desc) {
 }
 
 // One batch of pieces per thread (14336 x 4096 from bf16: quantise 24.6 us and read back 25.3, against 27.5 and 27.5
-// with 16 blocks per SM looping over single pieces; 22.7 is the floor of both).
+// with 16 blocks per SM looping over single pieces; 22.7 is the floor of both).  While all threads are resident
+// at once, one piece per thread (1000 x 1056 from fp32: 1.8 us, 2.2 in batches).
 static int mx4_grid(long chunks) {
-  constexpr long per_block = 256 * MX4_AT_ONCE;
+  const long per_block = chunks <= 256L * 8 * kNumSms ? 256 : 256 * MX4_AT_ONCE;
   return (int)std::min<long>((chunks + per_block - 1) / per_block, 1L << 24);
 }
 
