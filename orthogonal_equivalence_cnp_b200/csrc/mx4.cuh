@@ -600,34 +600,24 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   } else if (warp == MX4_CONV_WARPS + 1) {
     // ---------------- MMA issuer.  Its scheduler also serves converter warps, so that every instruction between two
     // products costs several cycles: the descriptors' low words are sums with constants, one barrier says that both
-    // operands are there, and one commit frees both.  (With two of each, and whole descriptors built per
-    // product, a step's issue took 1300 cycles, longer than its products: 52.9 us against 44 for 2048 tokens.)
+    // operands are there, and one commit frees both.  (With two of each, and whole descriptors built per product,
+    // a step's issue took 1300 cycles, more than its 1024 of products: 52.7 us for 2048 tokens of 4096 x 4096 against
+    // 50.2, 26.0 for 64 tokens of 4096 x 14336 against 21.4.  One lane walking the steps alone: 51.2 and 24.0.)
     const uint32_t idesc = idesc_bf16_f32(128, a.TN, ADJ, false);
-    const bool leader = elect_one();
     // A weight tile: MH = 2, 128 features (16 KiB) after the other; MH = 1, forward 64 positions after the other,
     // adjoint 64 features after the other.
     const uint64_t wd0 = ADJ ? smem_desc_sw128(sw, BK * 128, 1024) : smem_desc_sw128(sw, 16, 1024);
     const uint64_t xd0 = smem_desc_sw128(sw + W_BYTES, 16, 1024);
     const uint32_t w_hi = (uint32_t)(wd0 >> 32), x_hi = (uint32_t)(xd0 >> 32);
     uint32_t w_lo = (uint32_t)wd0, x_lo = (uint32_t)xd0;  // addresses in units of 16 bytes: they never carry
+    // The whole warp walks the steps, so that descriptors stay uniform, and one lane issues.
+    const bool leader = elect_one();
     int t = 0;
     uint32_t phase = 0;
     for (int i = 0; i < nkt; ++i) {
       if (!__all_sync(0xffffffffu, mbar_wait(ready(t), phase, KID_MX4, 2))) break;
       tc_fence_after();
-      if (leader) {
-#pragma unroll
-        for (int kk = 0; kk < BK / 16; ++kk) {
-          const uint32_t xl = x_lo + (kk >= 4 ? xa_bytes >> 4 : 0u) + (kk & 3) * 2;
-#pragma unroll
-          for (int h = 0; h < MH; ++h) {
-            const uint32_t wl = w_lo + (ADJ ? h * 1024 + kk * 128 : (h + (kk >> 2)) * 1024 + (kk & 3) * 2);
-            mma_bf16_words(tmem + (uint32_t)(h * a.TN), wl, w_hi, xl, x_hi, idesc, kk > 0 || i > 0);
-          }
-        }
-        mma_commit(taken(t));
-      }
-      __syncwarp();
+      const uint32_t bar = taken(t), w = w_lo, x = x_lo;
       w_lo += slot_bytes >> 4;
       x_lo += slot_bytes >> 4;
       if (++t == a.slots) {
@@ -636,6 +626,19 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
         w_lo = (uint32_t)wd0;
         x_lo = (uint32_t)xd0;
       }
+      if (leader) {
+#pragma unroll
+        for (int kk = 0; kk < BK / 16; ++kk) {
+          const uint32_t xl = x + (kk >= 4 ? xa_bytes >> 4 : 0u) + (kk & 3) * 2;
+#pragma unroll
+          for (int h = 0; h < MH; ++h) {
+            const uint32_t wl = w + (ADJ ? h * 1024 + kk * 128 : (h + (kk >> 2)) * 1024 + (kk & 3) * 2);
+            mma_bf16_words(tmem + (uint32_t)(h * a.TN), wl, w_hi, xl, x_hi, idesc, kk > 0 || i > 0);
+          }
+        }
+        mma_commit(bar);
+      }
+      __syncwarp();
     }
     if (leader) mma_commit(accum);
   } else {
@@ -645,7 +648,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     constexpr int ROWS = ADJ ? BK : 128 * MH;
     const int row = ct & (ROWS - 1), piece = ct / ROWS;  // row of a step's codes, 64 columns of it
     const int key = row & 7;                             // 128-byte swizzle of the bf16 tile
-    const uint32_t dst = (uint32_t)(piece * ROWS * 128 + row * 128);
+    const uint32_t dst = (uint32_t)(piece * ROWS * 128 + row * 128 + (key << 4));
     // Code tile: its 16-byte pieces are swizzled over 128 or 64 bytes; this group's step of it.
     constexpr int CROW = mx4_code_row(MH, ADJ);
     static_assert(CROW == 128 || CROW == 64, "swizzle widths");
@@ -656,31 +659,41 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     // The two scales of a step in 16 bits, loaded eight steps ahead (from HBM that is some 2 us: two steps ahead, their
     // latency set the pace of small token tiles).  Rows and features past the end repeat the last
     // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
-    const int nblock = (int)a.pitch, base = ADJ ? m0 / 32 + 2 * piece : 0;
-    const uint8_t* srow = ADJ ? a.scales : a.scales + (long)min(m0 + row, a.M - 1) * a.pitch;
+    const int nblock = (int)a.pitch;
     const bool even = a.pitch % 2 == 0;
-    auto load_scales = [&](int i) -> uint32_t {
+    const uint8_t* scale_at;
+    long scale_step;        // from one step of this group to the next
+    int scales_left, two_left;  // steps of this group whose first, whose second scale lies before the end
+    if (!ADJ) {
+      const int c = (kt0 + group) * (BK / 32) + 2 * piece, step = CS * (BK / 32);
+      scale_at = a.scales + (long)min(m0 + row, a.M - 1) * a.pitch + c;
+      scale_step = step;
+      scales_left = (nblock - c + step - 1) / step;
+      two_left = (nblock - c - 1 + step - 1) / step;
+    } else {
+      const int k = (kt0 + group) * BK + row;
+      const int base = even ? min(m0 / 32 + 2 * piece, nblock - 2) : min(m0 / 32 + 2 * piece, nblock - 1);
+      scale_at = a.scales + (long)k * a.pitch + base;
+      scale_step = (long)CS * BK * a.pitch;
+      scales_left = (a.K - k + CS * BK - 1) / (CS * BK);
+      two_left = base + 1 < nblock ? scales_left : 0;
+    }
+    scales_left = min(scales_left, (nkt - group + CS - 1) / CS);
+    auto load_scales = [&]() -> uint32_t {
       uint32_t e = 127u | 127u << 8;
-      if (!ADJ) {
-        const int c = (kt0 + i) * (BK / 32) + 2 * piece;
-        if (i < nkt && c < nblock) {
-          if (even) e = __ldg(reinterpret_cast<const uint16_t*>(srow + c));
-          else e = (uint32_t)__ldg(srow + c) | (c + 1 < nblock ? (uint32_t)__ldg(srow + c + 1) : 127u) << 8;
-        }
-      } else {
-        const int k = (kt0 + i) * BK + row;
-        if (i < nkt && k < a.K) {
-          const uint8_t* at = srow + (long)k * a.pitch;
-          if (even) e = __ldg(reinterpret_cast<const uint16_t*>(at + min(base, nblock - 2)));
-          else e = (uint32_t)__ldg(at + min(base, nblock - 1)) | (uint32_t)__ldg(at + min(base + 1, nblock - 1)) << 8;
-        }
+      if (scales_left > 0) {
+        if (even) e = __ldg(reinterpret_cast<const uint16_t*>(scale_at));
+        else e = (uint32_t)__ldg(scale_at) | (two_left > 0 ? (uint32_t)__ldg(scale_at + 1) : 127u) << 8;
       }
+      scale_at += scale_step;
+      --scales_left;
+      --two_left;
       return e;
     };
     constexpr int AHEAD = 4;
     uint32_t next[AHEAD];
 #pragma unroll
-    for (int q = 0; q < AHEAD; ++q) next[q] = load_scales(group + CS * q);
+    for (int q = 0; q < AHEAD; ++q) next[q] = load_scales();
     int s = 0, t = group;  // at least two slots
     uint32_t s_phase = 0, t_phase = 1;
     bool ok = true;
@@ -690,24 +703,24 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
         const int i = i0 + CS * q;
         if (i >= nkt) break;
         const uint32_t scales = next[q];
-        next[q] = load_scales(i + CS * AHEAD);
+        next[q] = load_scales();
         ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
         const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
         ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t tile = sw + t * slot_bytes + dst;
+        const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row stands at position j ^ key of its 128 bytes
         const uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
         // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
         if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
           const Mx4Scale f[2] = {mx4_scale(scales & 0xFFu), mx4_scale(scales >> 8)};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8<!ADJ>(w[j], f[j >> 2]));
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile ^ (j << 4), mx4_decode8<!ADJ>(w[j], f[j >> 2]));
         } else {
           const uint32_t f1[2] = {(scales & 0xFFu) * 0x00800080u + 126u * 0x00800080u,
                                   (scales >> 8) * 0x00800080u + 126u * 0x00800080u};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile + ((j ^ key) << 4), mx4_decode8<!ADJ>(w[j], f1[j >> 2]));
+          for (int j = 0; j < 8; ++j) st_shared_v4(tile ^ (j << 4), mx4_decode8<!ADJ>(w[j], f1[j >> 2]));
         }
         fence_proxy_async_smem();  // the tensor core reads what the threads wrote
         __syncwarp();
@@ -718,8 +731,8 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
           mbar_arrive(cempty(s));
         }
         if (++s == a.cs) { s = 0; s_phase ^= 1u; }
-        for (int p = 0; p < CS; ++p)
-          if (++t == a.slots) { t = 0; t_phase ^= 1u; }
+        t += CS;
+        if (t >= a.slots) { t -= a.slots; t_phase ^= 1u; }
       }
     }
   }

@@ -271,6 +271,28 @@ def test_products_on_streams_and_in_a_graph():
     device_clean()
 
 
+@pytest.mark.parametrize("adjoint,n,d_in,d_out", [(1, 64, 4096, 14336), (0, 64, 4096, 4096), (1, 33, 1024, 14336),
+                                                  (0, 500, 4096, 1024), (1, 2048, 4096, 4096), (0, 1, 4096, 4096)])
+def test_products_with_cold_caches(adjoint, n, d_in, d_out):
+    # Everything from HBM, the rings of tiles gone round many times: a tile given back before it is read, or read
+    # before it has arrived, shows only with such latencies.
+    X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, 11)
+    W = _weight64(codes, scales)
+    ref = (X.double() @ (W if adjoint else W.t())).to(torch.bfloat16)
+    flush = torch.empty(300 << 20, dtype=torch.uint8, device="cuda")  # larger than the L2 cache
+    Y = torch.empty_like(ref)
+    wrong = torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(25):
+        Y.zero_()
+        flush.fill_(i)
+        if i % 3 == 0:
+            torch.cuda.synchronize()
+        P.poetx_mx4_matmul(adjoint, n, d_in, d_out, X, codes, scales, Y)
+        wrong += (Y != ref).sum()
+    assert wrong.item() == 0
+    device_clean()
+
+
 def test_quantize_then_multiply_needs_no_wait():
     # Launched back to back on one stream: the product reads what the quantiser has just written.
     g = torch.Generator(device="cuda").manual_seed(4)
