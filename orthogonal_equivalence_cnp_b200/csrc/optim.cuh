@@ -91,14 +91,14 @@ __device__ __forceinline__ f32x2 both(float x) { return pair(x, x); }
 // it cannot know, a b + -0 is a b rounded, in the one instruction a product takes anyway.
 __device__ __forceinline__ f32x2 mul2_alone(f32x2 a, f32x2 b, float minus_zero) { return fma2(a, b, both(minus_zero)); }
 
-// 0 <= a <= 448 (or a rounding above) to the e4m3 grid, up with the probability of the part that is cut off (16
-// random bits; the bias is at most 2^-17 of a step).  From 2^-6 on the grid has 3 mantissa bits: the bits below
-// them are cut after the addition, which carries into the exponent where it should (beyond 448 the
-// conversion saturates).  Exact zero stays zero.
+// |a| <= 448 (or a rounding above) to the e4m3 grid, away from zero with the probability of the part that is cut off
+// (16 random bits; the bias is at most 2^-17 of a step); the sign is a bit of its own and stays.  From 2^-6 on the grid
+// has 3 mantissa bits: the bits below them are cut after the addition, which carries into the exponent where it
+// should (beyond 448 the conversion saturates).  Exact zero stays zero.
 __device__ __forceinline__ float e4m3_stochastic(float a, uint32_t rnd16) {
   return __uint_as_float((__float_as_uint(a) + (rnd16 << 4)) & 0xFFF00000u);
 }
-// The same under 2^-6, where the grid is the multiples of 2^-9: floor(512 a + rnd / 2^16), the floor by adding
+// The same for 0 <= a < 2^-6, where the grid is the multiples of 2^-9: floor(512 a + rnd / 2^16), the floor by adding
 // 2^23 rounded down (exact for these sizes, and no slow conversion instruction).
 __device__ __forceinline__ float e4m3_stochastic_small(float a, uint32_t rnd16) {
   const float r = __uint_as_float(0x3F800000u | (rnd16 << 7)) - 1.f;
@@ -121,6 +121,32 @@ __device__ __forceinline__ f32x2 sqrt2_normal(f32x2 v) {
   const f32x2 y = pair(rsqrt_approx(a), rsqrt_approx(b));
   const f32x2 s = mul2(v, y);
   return fma2(fma2(mul2(s, both(-1.f)), s, v), mul2(both(0.5f), y), s);
+}
+// Largest magnitude and largest of three, a NaN on top; smallest magnitude and smallest of three.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3_abs(float a, float b, float c) {
+  float d;
+  asm("min.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -157,6 +183,10 @@ __device__ __forceinline__ void store4(void* base, long i, const float (&x)[4]) 
     *reinterpret_cast<float4*>(static_cast<float*>(base) + i) = make_float4(x[0], x[1], x[2], x[3]);
   }
 }
+__device__ __forceinline__ uint2 pack4_bf16(const float (&x)[4]) {
+  const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+  return make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+}
 template <bool BF>
 __device__ __forceinline__ void store4_tail(void* base, long i, long n, const float (&x)[4]) {
 #pragma unroll
@@ -190,51 +220,45 @@ __device__ __forceinline__ uint32_t encode4(const float (&q)[4]) {
   return lo | (hi << 16);
 }
 
-// Four codes of |x| * inv with x's sign; POSITIVE (the root of a second moment): a positive value
-// gets at least the smallest code, since m / (0 + eps) must not happen where gradients were seen.
-// Values under 2^-6 of the grid are rare (3.5e-5 of the block's largest), so they take a branch.
+// Four codes of x * inv.  POSITIVE (the root of a second moment): a positive value gets at least the smallest
+// code, since m / (0 + eps) must not happen where gradients were seen.  Values under 2^-6 of the grid are rare
+// (3.5e-5 of the block's largest), so they take a branch.
 template <bool POSITIVE>
 __device__ __forceinline__ uint32_t encode_moments(const float (&x)[4], float inv, bool stochastic,
                                                    const uint32_t (&h)[4]) {
   float q[4];
   unpair(mul2(pair(x[0], x[1]), both(inv)), q[0], q[1]);
   unpair(mul2(pair(x[2], x[3]), both(inv)), q[2], q[3]);
+  if (__builtin_expect(fminf(min3_abs(q[0], q[1], q[2]), fabsf(q[3])) < 0.015625f, 0)) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) q[e] = fabsf(q[e]);
-  if (stochastic) {
-    if (fminf(fminf(q[0], q[1]), fminf(q[2], q[3])) < 0.015625f) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < 4; ++e) {
+      if (stochastic) {
         const uint32_t r = POSITIVE ? element_high16(h[e]) : element_low16(h[e]);
-        q[e] = q[e] < 0.015625f ? e4m3_stochastic_small(q[e], r) : e4m3_stochastic(q[e], r);
+        q[e] = copysignf(fabsf(q[e]) < 0.015625f ? e4m3_stochastic_small(fabsf(q[e]), r) : e4m3_stochastic(fabsf(q[e]), r),
+                         x[e]);
       }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        q[e] = e4m3_stochastic(q[e], POSITIVE ? element_high16(h[e]) : element_low16(h[e]));
+      if (POSITIVE && x[e] > 0.f) q[e] = fmaxf(q[e], 0.001953125f);
     }
-  }
+  } else if (stochastic) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    if (!POSITIVE) q[e] = copysignf(q[e], x[e]);
-    else if (x[e] > 0.f) q[e] = fmaxf(q[e], 0.001953125f);
+    for (int e = 0; e < 4; ++e) q[e] = e4m3_stochastic(q[e], POSITIVE ? element_high16(h[e]) : element_low16(h[e]));
   }
   return encode4(q);
 }
 
-// Eight elements of one thread: 4 at i0 and 4 at i0 + 128 of the warp's 256-element block.
-template <bool PBF, bool GBF, bool E4M3>
+// Eight elements of one thread: 4 at i0 and 4 at i0 + 128 of the warp's 256-element block.  FULL: all of the
+// block's elements exist.
+template <bool PBF, bool GBF, bool E4M3, bool FULL>
 __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg& a, long block, int lane) {
   const long i0 = block * kMomentBlock + 4 * lane;
-  const bool full = (block + 1) * kMomentBlock <= t.n;
   uint8_t* const cm = static_cast<uint8_t*>(t.m);
   uint8_t* const cv = static_cast<uint8_t*>(t.v);
   float p[2][4], g[2][4], m[2][4], v[2][4];
   uint32_t wm[2] = {0u, 0u}, wv[2] = {0u, 0u};
   float2 u = make_float2(0.f, 0.f);
-  if (full) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h) {
+    if (FULL) {
       load4<PBF>(t.p, i0 + 128 * h, p[h]);
       load4<GBF>(t.g, i0 + 128 * h, g[h]);
       if (E4M3) {
@@ -244,10 +268,7 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
         load4<false>(t.m, i0 + 128 * h, m[h]);
         load4<false>(t.v, i0 + 128 * h, v[h]);
       }
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    } else {
       load4_tail<PBF>(t.p, i0 + 128 * h, t.n, p[h]);
       load4_tail<GBF>(t.g, i0 + 128 * h, t.n, g[h]);
       if (E4M3) {
@@ -262,8 +283,7 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
   if (E4M3) u = t.scale[block];
   const bool stochastic = a.stochastic != 0;
   const float shrink = t.eta * t.decay, rate = t.eta * a.inv_bc1;
-  // Largest magnitudes as integers, which order as the floats do and put infinities and NaN on top.
-  uint32_t top_m = 0u, top_r = 0u;
+  float top_m = 0.f, top_r = 0.f;  // largest magnitudes, a NaN on top
   uint32_t rnd[2][4] = {};
   // The moments take one rounding per operation (no contraction), so that the codes are a
   // function of the inputs that a float32 restatement reproduces bit for bit.
@@ -290,9 +310,9 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
       unpair(m2[q], m[h][2 * q], m[h][2 * q + 1]);
       unpair(r2[q], v[h][2 * q], v[h][2 * q + 1]);
     }
-    const float low = fminf(fminf(v[h][0], v[h][1]), fminf(v[h][2], v[h][3]));
-    const float high = fmaxf(fmaxf(v[h][0], v[h][1]), fmaxf(v[h][2], v[h][3]));
-    if (low >= kSqrtLow && high <= kMaxFinite) {
+    const float low = fminf(min3(v[h][0], v[h][1], v[h][2]), v[h][3]);
+    const float high = fmaxf(max3(v[h][0], v[h][1], v[h][2]), v[h][3]);
+    if (__builtin_expect(low >= kSqrtLow && high <= kMaxFinite, 1)) {
       r2[0] = sqrt2_normal(r2[0]);
       r2[1] = sqrt2_normal(r2[1]);
     } else {
@@ -308,82 +328,106 @@ __device__ __forceinline__ void adamw_block(const MultiTensor& t, const MultiCfg
       const f32x2 th = pair(p[h][2 * q], p[h][2 * q + 1]);
       unpair(fma2(fma2(both(shrink), th, up), both(-1.f), th), p[h][2 * q], p[h][2 * q + 1]);
     }
+    if (stochastic && (E4M3 || PBF)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (stochastic && (E4M3 || PBF)) rnd[h][e] = element_bits(i0 + 128 * h, e, t.salt);
-      if (PBF && stochastic && p[h][e] == p[h][e]) {  // an infinity keeps its bits under this addition
-        const uint32_t b = element_finish(rnd[h][e]) * 0xBB67AE85u;
-        p[h][e] = __uint_as_float((__float_as_uint(p[h][e]) + (b >> 16)) & 0xFFFF0000u);
-      }
-      if (E4M3) {
-        v[h][e] = r[e];
-        top_m = max(top_m, __float_as_uint(fabsf(m[h][e])));
-        top_r = max(top_r, __float_as_uint(r[e]));
+      for (int e = 0; e < 4; ++e) rnd[h][e] = element_bits(i0 + 128 * h, e, t.salt);
+    }
+    uint2 pw = make_uint2(0u, 0u);  // bf16 parameters
+    if (PBF) {
+      const float any = max3_abs_nan(max3_abs_nan(p[h][0], p[h][1], p[h][2]), p[h][3], 0.f);
+      if (stochastic && __builtin_expect(any == any, 1)) {
+        // Random bits under the last one kept, the upper halves of the sums (an infinity keeps its bits).
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = __float_as_uint(p[h][e]) + ((element_finish(rnd[h][e]) * 0xBB67AE85u) >> 16);
+        pw = make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+      } else {
+        if (stochastic) {  // a NaN stays one; its neighbours are rounded as ever
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (p[h][e] == p[h][e])
+              p[h][e] = __uint_as_float((__float_as_uint(p[h][e]) + ((element_finish(rnd[h][e]) * 0xBB67AE85u) >> 16)) &
+                                        0xFFFF0000u);
+        }
+        pw = pack4_bf16(p[h]);
       }
     }
-  }
-  if (full) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      store4<PBF>(t.p, i0 + 128 * h, p[h]);
+    if (FULL) {
+      if (PBF) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(t.p) + i0 + 128 * h) = pw;
+      else store4<false>(t.p, i0 + 128 * h, p[h]);
       if (!E4M3) {
         store4<false>(t.m, i0 + 128 * h, m[h]);
         store4<false>(t.v, i0 + 128 * h, v[h]);
       }
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    } else {
+      if (PBF) {
+        p[h][0] = __uint_as_float(pw.x << 16); p[h][1] = __uint_as_float(pw.x & 0xFFFF0000u);
+        p[h][2] = __uint_as_float(pw.y << 16); p[h][3] = __uint_as_float(pw.y & 0xFFFF0000u);
+      }
       store4_tail<PBF>(t.p, i0 + 128 * h, t.n, p[h]);
       if (!E4M3) {
         store4_tail<false>(t.m, i0 + 128 * h, t.n, m[h]);
         store4_tail<false>(t.v, i0 + 128 * h, t.n, v[h]);
       }
     }
+    if (E4M3) {
+#pragma unroll
+      for (int e = 0; e < 4; e += 2) {
+        top_m = max3_abs_nan(top_m, m[h][e], m[h][e + 1]);
+        top_r = max3_nan(top_r, r[e], r[e + 1]);
+      }
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[h][e] = r[e];
+    }
   }
   if (!E4M3) return;
-  top_m = __reduce_max_sync(0xffffffffu, top_m);
-  top_r = __reduce_max_sync(0xffffffffu, top_r);
+  // Bit patterns of magnitudes order as the numbers do, infinities and NaN on top.
+  uint32_t most_m = __reduce_max_sync(0xffffffffu, __float_as_uint(top_m));
+  uint32_t most_r = __reduce_max_sync(0xffffffffu, __float_as_uint(top_r));
   uint32_t bad_m[2] = {0u, 0u}, bad_r[2] = {0u, 0u};
-  if (max(top_m, top_r) >= 0x7F800000u) {
+  if (__builtin_expect(max(most_m, most_r) >= 0x7F800000u, 0)) {
     // A NaN or an infinity is left out of the block's maximum and stored as the NaN code.
-    top_m = top_r = 0u;
+    most_m = most_r = 0u;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         if (!(fabsf(m[h][e]) <= kMaxFinite)) { bad_m[h] |= 0x7Fu << (8 * e); m[h][e] = 0.f; }
         if (!(v[h][e] <= kMaxFinite)) { bad_r[h] |= 0x7Fu << (8 * e); v[h][e] = 0.f; }
-        top_m = max(top_m, __float_as_uint(fabsf(m[h][e])));
-        top_r = max(top_r, __float_as_uint(v[h][e]));
+        most_m = max(most_m, __float_as_uint(fabsf(m[h][e])));
+        most_r = max(most_r, __float_as_uint(v[h][e]));
       }
-    top_m = __reduce_max_sync(0xffffffffu, top_m);
-    top_r = __reduce_max_sync(0xffffffffu, top_r);
+    most_m = __reduce_max_sync(0xffffffffu, most_m);
+    most_r = __reduce_max_sync(0xffffffffu, most_r);
   }
-  // A block whose largest is under 2^-100 is stored as zeros (448 / top would overflow).
-  const float tm = __uint_as_float(top_m) < kSqrtLow ? 0.f : __uint_as_float(top_m);
-  const float tr = __uint_as_float(top_r) < kSqrtLow ? 0.f : __uint_as_float(top_r);
-  const float inv_m = tm > 0.f ? __fmul_rn(448.f, __frcp_rn(tm)) : 0.f;
-  const float inv_r = tr > 0.f ? __fmul_rn(448.f, __frcp_rn(tr)) : 0.f;
+  // A block whose largest is under 2^-100 is stored as zeros (448 / top would overflow).  Odd lanes divide for the
+  // roots, even ones for the first moments.
+  const float top = __uint_as_float(lane & 1 ? most_r : most_m);
+  const float tops = top < kSqrtLow ? 0.f : top;
+  const float inv = tops > 0.f ? __fmul_rn(448.f, __frcp_rn(tops)) : 0.f;
+  const float inv_m = __shfl_sync(0xffffffffu, inv, 0), inv_r = __shfl_sync(0xffffffffu, inv, 1);
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     wm[h] = encode_moments<false>(m[h], inv_m, stochastic, rnd[h]) | bad_m[h];
     wv[h] = encode_moments<true>(v[h], inv_r, stochastic, rnd[h]) | bad_r[h];
   }
-  if (full) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < 2; ++h) {
+    if (FULL) {
       *reinterpret_cast<uint32_t*>(cm + i0 + 128 * h) = wm[h];
       *reinterpret_cast<uint32_t*>(cv + i0 + 128 * h) = wv[h];
-    }
-  } else {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    } else {
       store_codes4_tail(cm, i0 + 128 * h, t.n, wm[h]);
       store_codes4_tail(cv, i0 + 128 * h, t.n, wv[h]);
     }
   }
-  if (lane == 0) t.scale[block] = make_float2(__fmul_rn(tm, 1.f / 448.f), __fmul_rn(tr, 1.f / 448.f));
+  if (lane < 2) reinterpret_cast<float*>(t.scale + block)[lane] = __fmul_rn(tops, 1.f / 448.f);
+}
+
+template <bool PBF, bool GBF, bool E4M3>
+__device__ __forceinline__ void adamw_any(const MultiTensor& t, const MultiCfg& a, long block, int lane) {
+  if ((block + 1) * kMomentBlock <= t.n) adamw_block<PBF, GBF, E4M3, true>(t, a, block, lane);
+  else adamw_block<PBF, GBF, E4M3, false>(t, a, block, lane);
 }
 
 // Tiles of 2048 elements (eight 256-element blocks, one per warp) over all tensors.  Each block of threads
@@ -407,14 +451,14 @@ __global__ void __launch_bounds__(kMultiThreads, 4) adamw_multi_kernel(const __g
     const long block = (long)(tile - args.first[at]) * (kMultiTile / kMomentBlock) + warp;
     if (block * kMomentBlock >= t.n) continue;  // past the tensor's last block (the whole warp)
     switch (t.flags) {
-      case 0: adamw_block<false, false, false>(t, a, block, lane); break;
-      case 1: adamw_block<true, false, false>(t, a, block, lane); break;
-      case 2: adamw_block<false, true, false>(t, a, block, lane); break;
-      case 3: adamw_block<true, true, false>(t, a, block, lane); break;
-      case 4: adamw_block<false, false, true>(t, a, block, lane); break;
-      case 5: adamw_block<true, false, true>(t, a, block, lane); break;
-      case 6: adamw_block<false, true, true>(t, a, block, lane); break;
-      default: adamw_block<true, true, true>(t, a, block, lane); break;
+      case 0: adamw_any<false, false, false>(t, a, block, lane); break;
+      case 1: adamw_any<true, false, false>(t, a, block, lane); break;
+      case 2: adamw_any<false, true, false>(t, a, block, lane); break;
+      case 3: adamw_any<true, true, false>(t, a, block, lane); break;
+      case 4: adamw_any<false, false, true>(t, a, block, lane); break;
+      case 5: adamw_any<true, false, true>(t, a, block, lane); break;
+      case 6: adamw_any<false, true, true>(t, a, block, lane); break;
+      default: adamw_any<true, true, true>(t, a, block, lane); break;
     }
   }
 }

@@ -1343,10 +1343,17 @@ static poetx_status adamw_multi_launch(const poetx_adamw_cfg* cfg, const MultiCf
     }
     if (a.c.count == 0) break;
     auto kern = adamw_multi_kernel<MAX>;
-    int per_sm = 1;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMultiThreads, 0) != cudaSuccess)
-      return POETX_ERR_CUDA;
-    const uint32_t grid = std::min<uint32_t>(a.c.tiles, (uint32_t)(device_sms() * std::max(per_sm, 1)));
+    static std::atomic<int> resident[kMaxDevices];  // blocks per SM, asked once per device (0.4 us a call)
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return POETX_ERR_CUDA;
+    int per_sm = resident[dev].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+      if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kMultiThreads, 0) != cudaSuccess)
+        return POETX_ERR_CUDA;
+      per_sm = std::max(per_sm, 1);
+      resident[dev].store(per_sm, std::memory_order_relaxed);
+    }
+    const uint32_t grid = std::min<uint32_t>(a.c.tiles, (uint32_t)(device_sms() * per_sm));
     cudaLaunchConfig_t lc = {};
     lc.gridDim = dim3(grid);
     lc.blockDim = dim3(kMultiThreads);
