@@ -255,7 +255,8 @@ poetx_status poetx_mx4_dequantize(int rows, int cols, const uint8_t* codes, cons
  * the frozen part of a training step.
  *   adjoint = 0:  Y [n, d_out] = X [n, d_in] . W^T        adjoint = 1:  Y [n, d_in] = X [n, d_out] . W
  * X and Y bf16, row-major, not overlapping; sums in float32, rounded once.  d_in a multiple of 32, d_out of 8
- * (UNSUPPORTED_SHAPE otherwise).  n_tokens == 0 launches nothing.  The same arguments give the same bits. */
+ * (UNSUPPORTED_SHAPE otherwise).  n_tokens == 0 launches nothing.  The same arguments give the same bits; the order of
+ * a token's sums, and so its last bits, may change with n_tokens. */
 poetx_status poetx_mx4_matmul(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
                               const uint8_t* scales, void* Y, poetx_stream stream);
 
@@ -372,7 +373,7 @@ poetx_status poetx_adamw_reset(long long n, float* m, float* v, poetx_stream str
  * seed == 0 rounds codes and bf16 parameters to nearest, ties to even.  seed != 0 rounds them up with the
  * probability of the part cut off, from 16 bits of a hash of (seed, position in `tensors`, element): with a
  * new seed each step, changes below half a step of the grid (as (1 - beta2) makes them) add up instead of
- * being lost.  The same arguments give the same bits. */
+ * being lost.  The same arguments give the same bits; a captured call keeps its cfg, t and seed in every replay. */
 #define POETX_MOMENT_BLOCK 256
 typedef enum { POETX_MOMENT_F32 = 0, POETX_MOMENT_E4M3 = 1 } poetx_moment;
 typedef struct {

@@ -235,9 +235,16 @@ bool make_tmap(CUtensorMap* m, const Operand& op, uint32_t box_inner, uint32_t b
   const CUtensorMapDataType type = dt == F32  ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
                                    : dt == U8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                               : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  return fn(m, type, 2, const_cast<void*>(op.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            dt == U8 ? u8_swizzle : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  auto encode = [&] {
+    return fn(m, type, 2, const_cast<void*>(op.base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              dt == U8 ? u8_swizzle : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  };
+  if (encode()) return true;
+  // A host thread that has made no runtime call yet has no current context for this driver call; choosing the
+  // device it is on anyway binds one.
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
 template <int BN, int ST, bool AMN, bool BMN>

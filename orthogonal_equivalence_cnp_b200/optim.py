@@ -102,7 +102,8 @@ class MultiAdamW:
 
     def step(self, cfg: poetx_adamw_cfg, t: Optional[int] = None, seed: int = 0, stream=None):
         """One step.  t: the moments' step count (default: one more than the last step's).  seed: 0
-        rounds to nearest, another (a new one each step) rounds stochastically."""
+        rounds to nearest, another (a new one each step) rounds stochastically.  Under stream capture cfg, t
+        and seed are kept by the graph: every replay is the same step."""
         t = self.t + 1 if t is None else t
         if self._device is not None and self._device.index != torch.cuda.current_device():
             with torch.cuda.device(self._device):

@@ -126,7 +126,8 @@ def _weight64(codes, scales):
     return lut[c.long()] * s
 
 
-SHAPES = [(32, 8), (32, 128), (64, 136), (96, 1000), (1056, 264), (992, 256), (4096, 512), (320, 4096), (2080, 40)]
+SHAPES = [(32, 8), (32, 128), (64, 136), (96, 1000), (1056, 264), (992, 256), (4096, 512), (320, 4096), (2080, 40),
+          (32768, 24), (64, 32776)]
 TOKENS = [1, 2, 7, 8, 9, 16, 17, 31, 33, 64, 65, 127, 200, 257, 600]
 
 
@@ -268,6 +269,105 @@ def test_products_on_streams_and_in_a_graph():
     torch.cuda.synchronize()
     for c in cases:
         assert torch.equal(c[7], -c[8])
+    device_clean()
+
+
+@pytest.mark.parametrize("n,d_in,d_out", [(3, 96, 40), (70, 256, 264), (300, 1056, 1000)])
+def test_adjoint_is_the_transpose_of_the_forward_product(n, d_in, d_out):
+    # <dY, X W^T> = <dY W, X>, and the derivative of <dY, Y(X)> along any direction: exact with numbers this small
+    # (sparse -1, 0, 1 on both sides, codes of -1, 0, 1: every output an integer under 256, exact in bf16).
+    g = torch.Generator(device="cuda").manual_seed(n)
+
+    def sparse(rows, cols, p):
+        return (torch.randint(-1, 2, (rows, cols), device="cuda", generator=g)
+                * (torch.rand(rows, cols, device="cuda", generator=g) < p)).to(torch.bfloat16)
+
+    nib = torch.tensor([0, 2, 10], device="cuda")[torch.randint(0, 3, (d_out, d_in), device="cuda", generator=g)]
+    codes = (nib[:, 0::2] + 16 * nib[:, 1::2]).to(torch.uint8)
+    scales = torch.full((d_out, d_in // 32), 127, dtype=torch.uint8, device="cuda")
+    X, D, dY = sparse(n, d_in, 0.2), sparse(n, d_in, 0.2), sparse(n, d_out, 0.2)
+    dX = _matmul(1, dY, codes, scales, d_in, d_out)
+    assert dX.abs().max().item() <= 256
+    f = lambda x: (dY.double() * _matmul(0, x, codes, scales, d_in, d_out).double()).sum().item()
+    assert f(X) == (dX.double() * X.double()).sum().item()
+    assert (f(X + D) - f(X - D)) / 2 == (dX.double() * D.double()).sum().item()
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("n,d_in,d_out", [(1, 96, 56), (9, 1056, 1000), (40, 1056, 1000), (300, 512, 264)])
+def test_arrays_that_start_on_16_bytes_only(adjoint, n, d_in, d_out):
+    X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, 21)
+    W = _weight64(codes, scales)
+    ref = (X.double() @ (W if adjoint else W.t())).to(torch.bfloat16)
+
+    def shifted(t):  # the same values 16 bytes into a buffer, with 16 bytes behind
+        flat = torch.zeros(t.numel() * t.element_size() + 32, dtype=torch.uint8, device="cuda")
+        assert flat.data_ptr() % 256 == 0
+        v = flat[16:-16].view(t.dtype).view(t.shape)
+        v.copy_(t)
+        return flat, v
+
+    bx, x = shifted(X)
+    bc, c = shifted(codes)
+    bs, sc = shifted(scales)
+    by, y = shifted(torch.zeros_like(ref))
+    by[:16] = by[-16:] = 77
+    P.poetx_mx4_matmul(adjoint, n, d_in, d_out, x, c, sc, y)
+    assert torch.equal(y, ref)
+    assert (by[:16] == 77).all().item() and (by[-16:] == 77).all().item()
+    bw, w = shifted(torch.zeros(d_out, d_in, dtype=torch.bfloat16, device="cuda"))
+    bw[:16] = bw[-16:] = 77
+    P.poetx_mx4_dequantize(d_out, d_in, c, sc, w)
+    assert torch.equal(w, W.to(torch.bfloat16))
+    P.poetx_mx4_quantize(P.POETX_BF16, d_out, d_in, w, c, sc)
+    back = torch.empty(d_out, d_in, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_dequantize(d_out, d_in, c, sc, back)
+    assert torch.equal(back, w) and (bw[:16] == 77).all().item() and (bw[-16:] == 77).all().item()
+    device_clean()
+
+
+def test_same_buffers_from_two_graphs_and_threads():
+    # Two graphs of the same call, replayed in turn and at once on two streams (same inputs, two outputs), and two host threads.
+    import threading
+    n, d_in, d_out = 100, 1056, 1000
+    X, codes, scales = _integer_problem(n, d_in, d_out, 0, 8)
+    ref = (X.double() @ _weight64(codes, scales).t()).to(torch.bfloat16)
+    Ys = [torch.zeros(n, d_out, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    P.poetx_mx4_matmul(0, n, d_in, d_out, X, codes, scales, Ys[0])
+    graphs = []
+    for Y in Ys:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            P.poetx_mx4_matmul(0, n, d_in, d_out, X, codes, scales, Y)
+        graphs.append(graph)
+    streams = [torch.cuda.Stream() for _ in Ys]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, stream in zip(graphs, streams):
+            with torch.cuda.stream(stream):
+                graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(Y, ref) for Y in Ys)
+
+    failed = []
+
+    def work(i):  # the first call of a thread is one that needs tensor maps
+        try:
+            for _ in range(50):
+                P.poetx_mx4_matmul(0, n, d_in, d_out, X, codes, scales, Ys[i], streams[i])
+        except Exception as e:
+            failed.append(e)
+
+    for Y in Ys:
+        Y.zero_()
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed and all(torch.equal(Y, ref) for Y in Ys)
     device_clean()
 
 
