@@ -161,7 +161,7 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// Up to 8 NT tokens.  The product is bound by reading the codes once (and by decoding them), so nothing is
+// 8 NT tokens a block.  For few tokens the product is bound by reading the codes once (and by decoding them), so nothing is
 // staged: every thread loads codes straight into the registers that the warp-level tensor instruction takes
 // them from.  The order of the K index inside an instruction is free as long as both operands agree, so a
 // thread takes the K positions whose codes lie together in memory.  The warps of a block, and the blocks of a
@@ -180,37 +180,57 @@ constexpr int MX4_FEW_COLS = 128;               // features of an adjoint block
 // Warps of a block.  One token, 4096 x 14336: forward 12.7 us with 4 warps and 4 blocks per SM, 13.5 with 8 and 2,
 // 14.9 with 16 rows a block; adjoint 17.7 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
 __host__ __device__ constexpr int mx4_few_warps(bool adj) { return adj ? 8 : 4; }
+// A warp's sums in shared memory: [token][feature], a feature's place and the tokens' stride such that both the
+// accumulators' stores (eight features 1 or 16 apart, four pairs of tokens) and the reads along the features meet
+// no bank twice.
+__host__ __device__ constexpr int mx4_few_stride(bool adj) { return adj ? 140 : 36; }
+template <bool ADJ>
+__device__ __forceinline__ int mx4_few_place(int feature) { return ADJ ? feature + (feature >> 4) : feature; }
 __host__ __device__ constexpr size_t mx4_few_smem(bool adj, int nt) {
-  return (size_t)mx4_few_warps(adj) * (adj ? MX4_FEW_COLS : MX4_FEW_ROWS) * 8 * nt * sizeof(float);
+  return (size_t)mx4_few_warps(adj) * mx4_few_stride(adj) * 8 * nt * sizeof(float);
 }
 
-// Sums red[warp][token][feature] over the warps and the cluster, rounds once, stores.
-template <int F, int T, int WARPS>
-__device__ __forceinline__ void mx4_few_finish(const Mx4FewArgs& a, float* red, int m0, int split) {
+// Sums the warps' results and the cluster's, rounds once, stores; two features at a time (M is even).
+template <bool ADJ, int T>
+__device__ __forceinline__ void mx4_few_finish(const Mx4FewArgs& a, float* red, int m0, int n0, int split) {
   using namespace sm100;
+  constexpr int F = ADJ ? MX4_FEW_COLS : MX4_FEW_ROWS, S = mx4_few_stride(ADJ), WARPS = mx4_few_warps(ADJ);
+  const int pairs = F / 2 * min(T, a.N - n0);
+  auto store = [&](int e, float lo, float hi) {
+    const int n = n0 + e / (F / 2), m = m0 + e % (F / 2) * 2;
+    if (m < a.M) *reinterpret_cast<uint32_t*>(a.Y + (size_t)n * a.M + m) = pack_bf16x2(lo, hi);
+  };
   __syncthreads();
-  for (int e = threadIdx.x; e < F * T; e += WARPS * 32) {
-    float x = red[e];
+  for (int e = threadIdx.x; e < pairs; e += WARPS * 32) {
+    float* at = red + e / (F / 2) * S;
+    const int f = e % (F / 2) * 2, f0 = mx4_few_place<ADJ>(f), f1 = mx4_few_place<ADJ>(f + 1);
+    float lo = at[f0], hi = at[f1];
 #pragma unroll
-    for (int w = 1; w < WARPS; ++w) x += red[w * F * T + e];
-    red[e] = x;
-  }
-  if (a.splits > 1) cluster_sync_all(); else __syncthreads();
-  const int share = F * T / a.splits;
-  for (int e = split * share + threadIdx.x; e < (split + 1) * share; e += WARPS * 32) {
-    const int n = e / F, m = m0 + e % F;
-    if (n < a.N && m < a.M) {
-      float x;
-      if (a.splits > 1) {
-        x = 0.f;
-        for (int r = 0; r < a.splits; ++r) x += ld_cluster_f32(mapa_shared(smem_u32(red + e), (uint32_t)r));
-      } else {
-        x = red[e];
-      }
-      a.Y[(size_t)n * a.M + m] = __float2bfloat16_rn(x);
+    for (int w = 1; w < WARPS; ++w) {
+      lo += at[w * T * S + f0];
+      hi += at[w * T * S + f1];
+    }
+    if (a.splits == 1) {
+      store(e, lo, hi);
+    } else {
+      at[f0] = lo;
+      at[f1] = hi;
     }
   }
-  if (a.splits > 1) cluster_sync_all();  // the peers have read this block's sums
+  if (a.splits == 1) return;
+  cluster_sync_all();
+  for (int e = pairs * split / a.splits + threadIdx.x; e < pairs * (split + 1) / a.splits; e += WARPS * 32) {
+    const int f = e % (F / 2) * 2;
+    const uint32_t at = smem_u32(red + e / (F / 2) * S);
+    const uint32_t a0 = at + 4 * mx4_few_place<ADJ>(f), a1 = at + 4 * mx4_few_place<ADJ>(f + 1);
+    float lo = 0.f, hi = 0.f;
+    for (int r = 0; r < a.splits; ++r) {
+      lo += ld_cluster_f32(mapa_shared(a0, (uint32_t)r));
+      hi += ld_cluster_f32(mapa_shared(a1, (uint32_t)r));
+    }
+    store(e, lo, hi);
+  }
+  cluster_sync_all();  // the peers have read this block's sums
 }
 
 // Forward: 32 features a block; a warp takes 128 input features at a time, thread (g, t) = (lane / 4, lane % 4) the
@@ -222,6 +242,7 @@ __global__ void __launch_bounds__(mx4_few_warps(false) * 32, 4) mx4_few_forward(
   constexpr int RT = MX4_FEW_RT, WARPS = mx4_few_warps(false);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_ROWS;
+  const int n0 = blockIdx.y * (8 * NT);
   const int nb = (a.K + 127) / 128;
   const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
   float acc[RT][NT][4] = {};
@@ -237,7 +258,7 @@ __global__ void __launch_bounds__(mx4_few_warps(false) * 32, 4) mx4_few_forward(
   }
   const __nv_bfloat16* x_at[NT];
 #pragma unroll
-  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(8 * u + g, a.N - 1) * a.K + 32 * t;
+  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(n0 + 8 * u + g, a.N - 1) * a.K + 32 * t;
   constexpr bool X_AHEAD = NT == 1;  // registers for 16 tokens' values are only there once
   struct Block {
     uint4 c[2 * RT], x[NT][4];
@@ -339,16 +360,22 @@ __global__ void __launch_bounds__(mx4_few_warps(false) * 32, 4) mx4_few_forward(
     use(k0);
   }
   griddep_launch();
-  constexpr int F = MX4_FEW_ROWS, T = 8 * NT;
-  float* out = red + (size_t)warp * F * T;
+  constexpr int T = 8 * NT, S = mx4_few_stride(false);
+  float* out = red + (size_t)warp * T * S;
+  const int live = a.N - n0;
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
+  for (int u = 0; u < NT; ++u)
 #pragma unroll
-    for (int u = 0; u < NT; ++u)
+    for (int q = 0; q < 2; ++q) {
+      const int token = 8 * u + 2 * t + q;
+      if (token < live)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        out[(8 * u + 2 * t + (q & 1)) * F + 16 * r + 8 * (q >> 1) + g] = acc[r][u][q];
-  mx4_few_finish<F, T, WARPS>(a, red, m0, split);
+        for (int r = 0; r < RT; ++r) {
+          out[token * S + 16 * r + g] = acc[r][u][q];
+          out[token * S + 16 * r + 8 + g] = acc[r][u][2 + q];
+        }
+    }
+  mx4_few_finish<false, T>(a, red, m0, n0, split);
 }
 
 // Adjoint: 128 features a block; a warp takes 16 rows of the weight at a time, thread (g, t) the codes of 16
@@ -360,6 +387,7 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
   constexpr int WARPS = mx4_few_warps(true);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int split = (int)(blockIdx.x % a.splits), m0 = (int)(blockIdx.x / a.splits) * MX4_FEW_COLS;
+  const int n0 = blockIdx.y * (8 * NT);
   const int nb = (a.K + 15) / 16;
   const int b_lo = (int)((long)nb * split / a.splits), b_hi = (int)((long)nb * (split + 1) / a.splits);
   float acc[8][NT][4] = {};
@@ -371,7 +399,7 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
   const uint8_t* scale_at = a.scales + (size_t)(4 * t) * spitch + mg / 32;
   const __nv_bfloat16* x_at[NT];
 #pragma unroll
-  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(8 * u + g, a.N - 1) * a.K + 4 * t;
+  for (int u = 0; u < NT; ++u) x_at[u] = a.X + (size_t)min(n0 + 8 * u + g, a.N - 1) * a.K + 4 * t;
   struct Block {
     uint2 c[4], x[NT];
     uint32_t e[4];
@@ -462,17 +490,23 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
     use(ring[0]);
   }
   griddep_launch();
-  constexpr int F = MX4_FEW_COLS, T = 8 * NT;
-  float* out = red + (size_t)warp * F * T;
+  constexpr int T = 8 * NT, S = mx4_few_stride(true);
+  float* out = red + (size_t)warp * T * S;
+  const int live = a.N - n0;
   // Accumulator row g of product j is feature 16 g + j, row g + 8 feature 16 g + 8 + j.
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int u = 0; u < NT; ++u)
 #pragma unroll
-    for (int u = 0; u < NT; ++u)
+    for (int q = 0; q < 2; ++q) {
+      const int token = 8 * u + 2 * t + q;
+      if (token < live)
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        out[(8 * u + 2 * t + (q & 1)) * F + 16 * g + 8 * (q >> 1) + j] = acc[j][u][q];
-  mx4_few_finish<F, T, WARPS>(a, red, m0, split);
+        for (int j = 0; j < 8; ++j) {
+          out[token * S + mx4_few_place<true>(16 * g + j)] = acc[j][u][q];
+          out[token * S + mx4_few_place<true>(16 * g + 8 + j)] = acc[j][u][2 + q];
+        }
+    }
+  mx4_few_finish<true, T>(a, red, m0, n0, split);
 }
 
 // -------------------------------------------------------------------------------- product, many tokens

@@ -529,11 +529,13 @@ poetx_status run_w_gemm_q8(const GemmDesc& g, const void* Q, long q_rows, bool q
 // ------------------------------------------------------------------------------ MX4 products
 struct Mx4Plan {
   int mh, tn, slots, cs, splits;
+  float us;  // predicted
 };
 // The tile (128 mh features, tn tokens) and the split of K with the least predicted time.  The prediction, in us,
 // is a fit to 560 measured combinations of 20 shapes (off by 10 % in the mean; its choice is at most 6 % slower than
 // the best measured one): per wave of blocks 2.6 to start, per step the larger of conversion (0.46, and
-// X's share of it) and products, and the epilogue, which a split makes dearer.  Clusters of 8 never paid.
+// X's share of it) and products, and the epilogue, which a split makes dearer.  Clusters of 8 never paid, and of
+// clusters of 4, one block per SM, 32 were resident at once while 35 took two waves.
 Mx4Plan mx4_plan(long M, long N, long K) {
   Mx4Plan p = {};
   float least = 0.f;
@@ -545,12 +547,12 @@ Mx4Plan mx4_plan(long M, long N, long K) {
       const long nt = (N + tile - 1) / tile;
       const int tn = (int)(((N + nt - 1) / nt + 15) / 16 * 16);  // evenly
       const float step = std::max(0.46f + 0.0006f * tn, 0.0025f * tn), end = 0.0066f * mh * tn;
-      for (int s = 1; s <= 4 && s <= kt && (s == 1 || mt * nt * s <= kNumSms); s *= 2) {
+      for (int s = 1; s <= 4 && s <= kt && (s == 1 || mt * nt * s <= (s == 2 ? kNumSms : 128)); s *= 2) {
         const float waves = (float)((mt * nt * s + kNumSms - 1) / kNumSms), steps = (float)((kt + s - 1) / s);
         const float t = waves * (2.6f + steps * step + end + (s > 1 ? 1.f + 0.023f * mh * tn : 0.f));
         if (p.mh == 0 || t < least) {
           least = t;
-          p.mh = mh; p.tn = tn; p.splits = s;
+          p.mh = mh; p.tn = tn; p.splits = s; p.us = t;
         }
       }
       if (nt == 1) break;
@@ -629,7 +631,7 @@ poetx_status launch_mx4_few(const Mx4FewArgs& a, cudaStream_t st, int cls) {
     attr_done[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((a.M + features - 1) / features * a.splits), 1, 1);
+  cfg.gridDim = dim3((unsigned)((a.M + features - 1) / features * a.splits), (unsigned)((a.N + 8 * NT - 1) / (8 * NT)), 1);
   cfg.blockDim = dim3(mx4_few_warps(ADJ) * 32, 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
@@ -647,7 +649,27 @@ poetx_status launch_mx4_few(const Mx4FewArgs& a, cudaStream_t st, int cls) {
   return last_launch();
 }
 
-constexpr int kMx4Few = 16;  // tokens up to which the product is read-bound: the kernels for few tokens
+// Blocks, split of K and predicted time of the kernels for few tokens.
+struct Mx4FewPlan {
+  int splits;
+  float us;
+};
+Mx4FewPlan mx4_few_plan(bool adjoint, long M, long N, long K) {
+  const long features = adjoint ? MX4_FEW_COLS : MX4_FEW_ROWS, warps = mx4_few_warps(adjoint), step = adjoint ? 16 : 128;
+  const long tiles = (M + features - 1) / features * ((N + 15) / 16), steps = (K + step - 1) / step;
+  Mx4FewPlan p;
+  // Split K over a cluster while the SMs have room for the warps and each of them has two steps (with
+  // one, 512 x 2048 takes 2.9 us split and 2.1 whole).
+  p.splits = 1;
+  while (p.splits < 8 && tiles * p.splits * 2 * warps <= 24L * kNumSms && steps >= 2 * warps * p.splits) p.splits *= 2;
+  // Fitted: per step that an SM takes on 0.175 us forward and 0.12 adjoint (16 tokens), or a warp's steps one after
+  // the other; the start; the cluster.
+  const float load = (float)(tiles * steps) / kNumSms, rounds = (float)((steps + warps * p.splits - 1) / (warps * p.splits));
+  p.us = 2.2f + (p.splits > 1 ? 0.8f : 0.f) +
+         (adjoint ? std::max(0.12f * load + 0.6f, 0.4f * rounds) : std::max(0.175f * load + 0.5f, 0.5f * rounds));
+  return p;
+}
+constexpr int kMx4Few = 16;  // tokens up to which the kernels for few tokens read the weight once: always theirs
 
 // Y [n, M] = X [n, K] . W^T (forward: M = d_out, K = d_in) or X . W (adjoint: M = d_in, K = d_out)
 // with W [d_out, d_in] in MX4.  Checked by the callers: aligned pointers, d_in a multiple of 32,
@@ -655,22 +677,20 @@ constexpr int kMx4Few = 16;  // tokens up to which the product is read-bound: th
 poetx_status mx4_product(bool adjoint, int n, int d_in, int d_out, const void* X, const uint8_t* codes,
                          const uint8_t* scales, void* Y, cudaStream_t st, int cls) {
   const int M = adjoint ? d_in : d_out, K = adjoint ? d_out : d_in;
-  if (n <= kMx4Few) {
-    const int features = adjoint ? MX4_FEW_COLS : MX4_FEW_ROWS;
-    const long tiles = ((long)M + features - 1) / features, blocks = (K + (adjoint ? 15 : 127)) / (adjoint ? 16 : 128);
+  const Mx4FewPlan few = mx4_few_plan(adjoint, M, n, K);
+  const Mx4Plan p = n <= kMx4Few ? Mx4Plan{} : mx4_plan(M, n, K);
+  // Small products beyond that too: the kernels for few tokens start faster and take no tensor maps (1 us of host
+  // time a call; half of it is counted).  1056 x 1000, 17 tokens forward: 4.3 us against 5.6; 300 tokens: 9.7
+  // against 7.3.  The adjoint only unsplit: its clusters cost it more than predicted (64 tokens: 7.1, 7.2).
+  if (n <= kMx4Few || (few.us < p.us + 0.5f && !(adjoint && few.splits > 1) && n <= 16 * 65535)) {
     Mx4FewArgs a;
     a.M = M; a.N = n; a.K = K;
+    a.splits = few.splits;
     a.X = static_cast<const __nv_bfloat16*>(X); a.codes = codes; a.scales = scales;
     a.Y = static_cast<__nv_bfloat16*>(Y);
-    // Split K over a cluster while the SMs have room for the warps and each of them has two steps (with
-    // one, 512 x 2048 takes 2.9 us split and 2.1 whole).
-    const long warps = mx4_few_warps(adjoint);
-    a.splits = 1;
-    while (a.splits < 8 && tiles * a.splits * 2 * warps <= 24L * kNumSms && blocks >= 2 * warps * a.splits) a.splits *= 2;
     if (adjoint) return n <= 8 ? launch_mx4_few<1, true>(a, st, cls) : launch_mx4_few<2, true>(a, st, cls);
     return n <= 8 ? launch_mx4_few<1, false>(a, st, cls) : launch_mx4_few<2, false>(a, st, cls);
   }
-  const Mx4Plan p = mx4_plan(M, n, K);
   const Operand x = view(X, n, K, K), c = view(codes, d_out, d_in / 2, d_in / 2);
   if (adjoint)
     return p.mh == 2 ? launch_mx4<2, true>(p, x, c, scales, Y, M, n, K, st, cls)

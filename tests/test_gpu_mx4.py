@@ -229,6 +229,15 @@ def test_product_offsets_past_32_bits():
     device_clean()
 
 
+@pytest.mark.parametrize("adjoint", [0, 1])
+def test_more_token_tiles_than_a_grid_has_rows(adjoint):
+    n, d_in, d_out = (1 << 20) + 5, 32, 8
+    X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, 4)
+    W = _weight64(codes, scales)
+    Y = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    assert torch.equal(Y, (X.double() @ (W if adjoint else W.t())).to(torch.bfloat16))
+
+
 def test_products_on_streams_and_in_a_graph():
     cases = []
     for i, (adjoint, n, d_in, d_out) in enumerate([(0, 1, 4096, 1024), (0, 33, 1056, 1000), (1, 300, 1056, 1000),
