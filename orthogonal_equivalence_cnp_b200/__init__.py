@@ -412,25 +412,31 @@ _mx4_types = None
 
 
 def _mx4_setup():
-    """Types of codes and scales (two weights a byte and E8M0, as uint8 or under torch's own names) and of values,
-    and the current device."""
+    """Types of codes and scales (two weights a byte and E8M0, as uint8 or under torch's own names) and of values."""
     global _mx4_types
     torch = _torch()
-    if _mx4_types is None:
-        _mx4_types = ((torch.uint8, torch.float4_e2m1fn_x2), (torch.uint8, torch.float8_e8m0fnu),
-                      (torch.bfloat16,), (torch.float32,))
-    return (*_mx4_types, torch.cuda.current_device() if torch.cuda.is_initialized() else 0)
+    _mx4_types = ((torch.uint8, torch.float4_e2m1fn_x2), (torch.uint8, torch.float8_e8m0fnu),
+                  (torch.bfloat16,), (torch.float32,))
+    return _mx4_types
+
+
+def _device():
+    """The current CUDA device, without initialising CUDA for it."""
+    torch = _torch_module or _torch()
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
 
 
 def _mx4(rows, cols, codes, scales):
     """Addresses of the codes and scales of a weight."""
-    ct, st, _, _, dev = _mx4_setup()
+    ct, st, _, _ = _mx4_types or _mx4_setup()
+    dev = _device()
     return (_array(codes, "codes", rows * cols // 2, ct, dev),
             _array(scales, "scales", rows * cols // POETX_MX4_BLOCK, st, dev))
 
 
 def poetx_mx4_quantize(dtype, rows, cols, W, codes, scales, stream=None):
-    ct, st, bf, f32, dev = _mx4_setup()
+    ct, st, bf, f32 = _mx4_types or _mx4_setup()
+    dev = _device()
     n = rows * cols
     w = _array(W, "W", n, bf if dtype == POETX_BF16 else f32, dev)
     c = _array(codes, "codes", n // 2, ct, dev)
@@ -441,7 +447,8 @@ def poetx_mx4_quantize(dtype, rows, cols, W, codes, scales, stream=None):
 
 
 def poetx_mx4_dequantize(rows, cols, codes, scales, W, stream=None):
-    ct, st, bf, _, dev = _mx4_setup()
+    ct, st, bf, _ = _mx4_types or _mx4_setup()
+    dev = _device()
     n = rows * cols
     c = _array(codes, "codes", n // 2, ct, dev)
     s = _array(scales, "scales", n // POETX_MX4_BLOCK, st, dev)
@@ -452,7 +459,8 @@ def poetx_mx4_dequantize(rows, cols, codes, scales, W, stream=None):
 
 
 def poetx_mx4_matmul(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, stream=None):
-    ct, st, bf, _, dev = _mx4_setup()
+    ct, st, bf, _ = _mx4_types or _mx4_setup()
+    dev = _device()
     n = d_out * d_in
     x = _array(X, "X", n_tokens * (d_out if adjoint else d_in), bf, dev)
     c = _array(codes, "codes", n // 2, ct, dev)

@@ -143,6 +143,17 @@ def test_products_of_small_integers_are_exact(adjoint, d_in, d_out):
 
 
 @pytest.mark.parametrize("adjoint", [0, 1])
+@pytest.mark.parametrize("n,d_in,d_out", [(600, 1056, 1000), (333, 4128, 1032), (1300, 2080, 3000), (2100, 4128, 4104),
+                                          (700, 14368, 264), (640, 96, 14344)])
+def test_large_products_whose_sides_fit_no_tile_are_exact(adjoint, n, d_in, d_out):
+    X, codes, scales = _integer_problem(n, d_in, d_out, adjoint, n)
+    Y = _matmul(adjoint, X, codes, scales, d_in, d_out)
+    W = _weight64(codes, scales)
+    ref = X.double() @ (W if adjoint else W.t())
+    assert torch.equal(Y, ref.to(torch.bfloat16)), (Y.double() - ref).abs().max().item()
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
 @pytest.mark.parametrize("n,d_in,d_out", [(1, 4096, 14336), (5, 14336, 4096), (40, 4096, 4096), (300, 1056, 1000),
                                           (2048, 4096, 4096), (2500, 4096, 2056), (4097, 2048, 4096)])
 def test_products_of_activations(adjoint, n, d_in, d_out):
