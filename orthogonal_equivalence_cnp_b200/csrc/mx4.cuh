@@ -161,9 +161,9 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], uint32_t a0, uint32_t a
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// 8 NT tokens a block.  For few tokens the product is bound by reading the codes once (and by decoding them), so nothing is
-// staged: every thread loads codes straight into the registers that the warp-level tensor instruction takes
-// them from.  The order of the K index inside an instruction is free as long as both operands agree, so a
+// 8 NT tokens a block.  For few tokens the product is bound by reading the codes once (and by decoding them), so
+// nothing is staged: every thread loads codes straight into the registers that the warp-level tensor instruction
+// takes them from.  The order of the K index inside an instruction is free as long as both operands agree, so a
 // thread takes the K positions whose codes lie together in memory.  The warps of a block, and the blocks of a
 // cluster, split K and add their sums in shared memory in a fixed order.
 struct Mx4FewArgs {
@@ -177,8 +177,9 @@ struct Mx4FewArgs {
 constexpr int MX4_FEW_RT = 2;                   // forward: 16-row tiles per block
 constexpr int MX4_FEW_ROWS = 16 * MX4_FEW_RT;   // features of a forward block
 constexpr int MX4_FEW_COLS = 128;               // features of an adjoint block
-// Warps of a block.  One token, 4096 x 14336: forward 12.7 us with 4 warps and 4 blocks per SM, 13.5 with 8 and 2,
-// 14.9 with 16 rows a block; adjoint 17.7 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
+// Warps of a block.  One token, 4096 x 14336 (31.2 MB of codes and scales, 4.8 us at the copy rate): forward 12.7 us
+// with 4 warps and 4 blocks per SM, 13.5 with 8 and 2, 14.9 with 16 rows a block (12.2, 2.6 TB/s, since the sums
+// meet no bank twice); adjoint 17.5 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
 __host__ __device__ constexpr int mx4_few_warps(bool adj) { return adj ? 8 : 4; }
 // A warp's sums in shared memory: [token][feature], a feature's place and the tokens' stride such that both the
 // accumulators' stores (eight features 1 or 16 apart, four pairs of tokens) and the reads along the features meet
@@ -519,9 +520,11 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 // products.  One warp streams X tiles and one the codes of MX4_CSTEPS steps at a time (whole 64- or 128-byte
 // rows: with rows of 32 bytes the copies took longer than the products) with TMA into rings; sixteen converter warps
 // turn a step's codes into a bf16 tile in the 128-byte-swizzled layout of the tensor core (forward: K-major, adjoint:
-// MN-major) in a ring of its own; one thread issues tcgen05.mma; the accumulators have features in TMEM lanes, tokens
-// in columns.  Where the tiles alone do not fill the SMs, a cluster of up to 8 CTAs splits K and each CTA sums its
-// share of the tokens over the cluster's shared memory, in a fixed order.
+// MN-major) in the slot that X's tile of the step lands in; one thread issues tcgen05.mma; the accumulators have
+// features in TMEM lanes, tokens in columns.  Where the tiles alone do not fill the SMs, a cluster of 2 or 4 CTAs splits
+// K and each CTA sums its share of the tokens over the cluster's shared memory, in a fixed order.
+// 2048 tokens, 4096 x 4096: 50.2 us (1.37 PFLOP/s; the tensor core is busy three quarters of the time) in short
+// runs, 59.9 in long ones under the power cap, where the library's product with a bf16 weight takes 56.1.
 struct Mx4Args {
   int M, N, K;           // features out, tokens, features in
   int TN, mt;            // tokens per tile; tiles along the features
@@ -690,13 +693,12 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     const uint32_t cpiece = (uint32_t)((ADJ ? 0 : 2 * KA * group) + 2 * piece);
     const uint32_t c0 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + ((cpiece ^ ckey) << 4);
     const uint32_t c1 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + (((cpiece + 1) ^ ckey) << 4);
-    // The two scales of a step in 16 bits, loaded eight steps ahead (from HBM that is some 2 us: two steps ahead, their
-    // latency set the pace of small token tiles).  Rows and features past the end repeat the last
+    // The two scales of a step in 16 bits, loaded eight steps ahead.  Rows and features past the end repeat the last
     // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
     const int nblock = (int)a.pitch;
     const bool even = a.pitch % 2 == 0;
     const uint8_t* scale_at;
-    long scale_step;        // from one step of this group to the next
+    long scale_step;            // from one step of this group to the next
     int scales_left, two_left;  // steps of this group whose first, whose second scale lies before the end
     if (!ADJ) {
       const int c = (kt0 + group) * (BK / 32) + 2 * piece, step = CS * (BK / 32);
@@ -743,7 +745,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
         ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row stands at position j ^ key of its 128 bytes
+        const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row: position j ^ key of its 128 bytes
         const uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
         // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
         if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
@@ -775,6 +777,11 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   // ---------------- epilogue
   bool ok = mbar_wait(accum, 0, KID_MX4, 6);
   ok = __all_sync(0xffffffffu, ok);
+  if (!ok) {
+    // Given up: copies still under way land within microseconds; they must find this block's memory.
+    for (const unsigned long long t0 = global_timer_ns(); global_timer_ns() - t0 < 1000000ull;) {
+    }
+  }
   tc_fence_after();
   griddep_launch();
   // The adjoint's features stand in mx4_decode8's order within each eight: this lane's.
@@ -799,7 +806,8 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) st_shared_b16(patch + ((8 * g + j) * 32 + feature) * 2, __float2bfloat16_rn(__uint_as_float(v[g][j])));
+            for (int j = 0; j < 8; ++j)
+              st_shared_b16(patch + ((8 * g + j) * 32 + feature) * 2, __float2bfloat16_rn(__uint_as_float(v[g][j])));
           __syncwarp();
 #pragma unroll
           for (int g = 0; g < 4; ++g) {
@@ -813,8 +821,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       }
     }
   } else {
-    // One 128-feature half after the other, fp32 sums through shared memory.
-    // red: fp32 [TN][128] at the start of the rings
+    // One 128-feature half after the other, fp32 sums [TN][128] through shared memory, at the start of the rings.
     const int share = a.TN / a.splits, c_lo = split * share;
 #pragma unroll 1
     for (int h = 0; h < MH; ++h) {
