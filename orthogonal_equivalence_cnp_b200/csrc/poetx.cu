@@ -558,9 +558,6 @@ Mx4Plan mx4_plan(long M, long N, long K) {
       if (nt == 1) break;
     }
   }
-#ifdef MX4_TUNE
-  if (const char* v = getenv("MX4P")) sscanf(v, "%d,%d,%d", &p.mh, &p.tn, &p.splits);
-#endif
   // Shared memory: four slots for the products where they fit, then code tiles, then more slots.
   auto slots_for = [&](int cs) {
     int n = MX4_MAX_RING;
