@@ -581,21 +581,15 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   uint32_t cols = 32;
   while (cols < (uint32_t)(MH * a.TN)) cols <<= 1;
 
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < a.slots; ++s) {
-      mbar_init(ready(s), MX4_GROUP / 32 + 1);  // the converting group's warps and X's copy
-      mbar_init(taken(s), 1);
-    }
-    for (int s = 0; s < a.cs; ++s) {
-      mbar_init(cfull(s), 1);
-      mbar_init(cempty(s), MX4_CONV_WARPS);
-    }
-    mbar_init(accum, 1);
+  if (threadIdx.x <= 4 * R) {
+    // One barrier per thread.  ready: the converting group's warps and X's copy; cempty: all converters.
+    const uint32_t kind = threadIdx.x / R;
+    mbar_init(sb + 8u * threadIdx.x, kind == 0 ? MX4_GROUP / 32 + 1 : kind == 3 ? MX4_CONV_WARPS : 1);
     fence_mbar_init();
     fence_proxy_async_smem();
-    prefetch_tmap(&tmX);
-    prefetch_tmap(&tmC);
   }
+  if (warp == MX4_CONV_WARPS + 1 && lane == 0) prefetch_tmap(&tmX);
+  if (warp == MX4_CONV_WARPS + 2 && lane == 0) prefetch_tmap(&tmC);
   if (warp == MX4_CONV_WARPS) {
     tmem_alloc(smem_u32(holder), cols);
     tmem_relinquish();
@@ -715,11 +709,20 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       two_left = base + 1 < nblock ? scales_left : 0;
     }
     scales_left = min(scales_left, (nkt - group + CS - 1) / CS);
-    auto load_scales = [&]() -> uint32_t {
-      uint32_t e = 127u | 127u << 8;
+    // Joined only when they are used (joining at the load waits for it: 1 us before the first step with odd pitches).
+    struct Pair {
+      uint32_t lo, hi;
+    };
+    auto load_scales = [&]() -> Pair {
+      Pair e = {127u, 127u};
       if (scales_left > 0) {
-        if (even) e = __ldg(reinterpret_cast<const uint16_t*>(scale_at));
-        else e = (uint32_t)__ldg(scale_at) | (two_left > 0 ? (uint32_t)__ldg(scale_at + 1) : 127u) << 8;
+        if (even) {
+          e.lo = __ldg(reinterpret_cast<const uint16_t*>(scale_at));
+          e.hi = 0u;
+        } else {
+          e.lo = __ldg(scale_at);
+          if (two_left > 0) e.hi = __ldg(scale_at + 1);
+        }
       }
       scale_at += scale_step;
       --scales_left;
@@ -727,7 +730,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       return e;
     };
     constexpr int AHEAD = 4;
-    uint32_t next[AHEAD];
+    Pair next[AHEAD];
 #pragma unroll
     for (int q = 0; q < AHEAD; ++q) next[q] = load_scales();
     int s = 0, t = group;  // at least two slots
@@ -738,7 +741,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       for (int q = 0; q < AHEAD; ++q) {
         const int i = i0 + CS * q;
         if (i >= nkt) break;
-        const uint32_t scales = next[q];
+        const uint32_t scales = next[q].lo | next[q].hi << 8;
         next[q] = load_scales();
         ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
         const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
