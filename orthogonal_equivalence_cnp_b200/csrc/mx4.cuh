@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     const uint32_t cpiece = (uint32_t)((ADJ ? 0 : 2 * KA * group) + 2 * piece);
     const uint32_t c0 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + ((cpiece ^ ckey) << 4);
     const uint32_t c1 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + (((cpiece + 1) ^ ckey) << 4);
-    // The two scales of a step in 16 bits, loaded eight steps ahead.  Rows and features past the end repeat the last
+    // The two scales of a step, loaded two steps ahead (eight cost a longer loop body: 2 % more time).  Rows and features past the end repeat the last
     // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
     const int nblock = (int)a.pitch;
     const bool even = a.pitch % 2 == 0;
@@ -729,50 +729,46 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       --two_left;
       return e;
     };
-    constexpr int AHEAD = 4;
-    Pair next[AHEAD];
-#pragma unroll
-    for (int q = 0; q < AHEAD; ++q) next[q] = load_scales();
+    Pair next = load_scales();
     int s = 0, t = group;  // at least two slots
     uint32_t s_phase = 0, t_phase = 1;
-    bool ok = true;
-    for (int i0 = group; i0 < nkt && ok; i0 += CS * AHEAD) {
-#pragma unroll  // so that a scale on its way is never moved between registers, which would wait for it
-      for (int q = 0; q < AHEAD; ++q) {
-        const int i = i0 + CS * q;
-        if (i >= nkt) break;
-        const uint32_t scales = next[q].lo | next[q].hi << 8;
-        next[q] = load_scales();
-        ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
-        const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
-        ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
-        const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row: position j ^ key of its 128 bytes
+    for (int i = group; i < nkt; i += CS) {
+      const uint32_t scales = next.lo | next.hi << 8;
+      next = load_scales();
+      bool ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
+      const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
+      ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row: position j ^ key of its 128 bytes
+      if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
+        // Scales above 2, which take a second product, are rare: a branch of the whole warp, kept small.
+#pragma unroll 1
+        for (int u = 0; u < 2; ++u) {
+          const Mx4Scale f = mx4_scale((scales >> (8 * u)) & 0xFFu);
+          const uint4 v = u ? c[1] : c[0];
+          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) st_shared_v4(tile ^ ((4 * u + j) << 4), mx4_decode8<!ADJ>(w[j], f));
+        }
+      } else {
         const uint32_t w[8] = {c[0].x, c[0].y, c[0].z, c[0].w, c[1].x, c[1].y, c[1].z, c[1].w};
-        // Scales above 2, which take a second product, are rare enough for a branch of the whole warp.
-        if (__any_sync(0xffffffffu, max(scales & 0xFFu, scales >> 8) > 128u)) {
-          const Mx4Scale f[2] = {mx4_scale(scales & 0xFFu), mx4_scale(scales >> 8)};
+        const uint32_t f1[2] = {(scales & 0xFFu) * 0x00800080u + 126u * 0x00800080u,
+                                (scales >> 8) * 0x00800080u + 126u * 0x00800080u};
 #pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile ^ (j << 4), mx4_decode8<!ADJ>(w[j], f[j >> 2]));
-        } else {
-          const uint32_t f1[2] = {(scales & 0xFFu) * 0x00800080u + 126u * 0x00800080u,
-                                  (scales >> 8) * 0x00800080u + 126u * 0x00800080u};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) st_shared_v4(tile ^ (j << 4), mx4_decode8<!ADJ>(w[j], f1[j >> 2]));
-        }
-        fence_proxy_async_smem();  // the tensor core reads what the threads wrote
-        __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(ready(t));
-          // Only now have the codes been used: given back right after their loads, before the wait above, a refill
-          // was seen to overtake the loads.
-          mbar_arrive(cempty(s));
-        }
-        if (++s == a.cs) { s = 0; s_phase ^= 1u; }
-        t += CS;
-        if (t >= a.slots) { t -= a.slots; t_phase ^= 1u; }
+        for (int j = 0; j < 8; ++j) st_shared_v4(tile ^ (j << 4), mx4_decode8<!ADJ>(w[j], f1[j >> 2]));
       }
+      fence_proxy_async_smem();  // the tensor core reads what the threads wrote
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(ready(t));
+        // Only now have the codes been used: given back right after their loads, before the wait above, a refill
+        // was seen to overtake the loads.
+        mbar_arrive(cempty(s));
+      }
+      if (++s == a.cs) { s = 0; s_phase ^= 1u; }
+      t += CS;
+      if (t >= a.slots) { t -= a.slots; t_phase ^= 1u; }
     }
   }
   __syncwarp();
