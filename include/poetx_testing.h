@@ -44,6 +44,16 @@ poetx_status poetx_test_gemm(int dtype, int M, int N, int K, int batch, int spli
  * ALIGNMENT, CUDA. */
 poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_stream stream);
 
+/* Failure-detection probe of the many-token MX4 product: poetx_mx4_matmul's tensor-core kernel with its waits bounded
+ * by limit_ns (1 us .. 100 ms), whose first block copies only the first `steps` steps of its codes (rounded up to
+ * pairs).  That block's waits run out: it records a device timeout (detail (9 << 8) | site) and returns
+ * with its tile of Y as it was, and so do the blocks of its cluster; every other tile is computed as ever.  *splits (a HOST int)
+ * receives the number of blocks of a cluster.  Errors as poetx_mx4_matmul, and INVALID_ARG (n_tokens <= 0, the limit out of
+ * range, as many steps as the block has). */
+poetx_status poetx_test_mx4_give_up(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
+                                    const uint8_t* scales, void* Y, int steps, long long limit_ns, int* splits,
+                                    poetx_stream stream);
+
 /* Compares the square root of the 8-bit moments with CUDA's correctly rounded one for the float32 numbers with the
  * bit patterns first..last, all from 2^-100 (0x0D800000) up to the largest finite one (0x7F7FFFFF);
  * *mismatches (device memory, 8-byte aligned) receives how many differ. */

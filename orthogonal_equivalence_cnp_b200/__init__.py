@@ -22,7 +22,7 @@ __all__ = [
     "poetx_xq_quantize", "poetx_xq_dequantize", "poetx_xq_forward", "poetx_xq_backward", "poetx_xq_merge",
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
-    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
+    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "poetx_test_mx4_give_up", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
     "poetx_mx4_quantize", "poetx_mx4_dequantize", "poetx_mx4_matmul", "poetx_mx4_forward", "poetx_mx4_backward",
     "poetx_mx4_merge", "POETX_MX4_BLOCK",
 ]
@@ -115,6 +115,7 @@ _SIGNATURES = {
     "poetx_fourperm_forward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_fourperm_backward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_test_wait_timeout": (_I, [_LL, _P, _P]),
+    "poetx_test_mx4_give_up": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _LL, ctypes.POINTER(_I), _P]),
     "poetx_test_sqrt": (_I, [ctypes.c_uint, ctypes.c_uint, _P, _P]),
     "poetx_status_string": (ctypes.c_char_p, [_I]),
     "poetx_device_status": (_I, [ctypes.POINTER(ctypes.c_int)]),
@@ -564,6 +565,19 @@ def poetx_cnp_blocks_noalloc(desc, n_blocks, theta, Q, stream=None):
 
 def poetx_test_wait_timeout(limit_ns, returned, stream=None):
     _check(lib().poetx_test_wait_timeout(int(limit_ns), _ptr(returned), _stream(stream)), "poetx_test_wait_timeout")
+
+
+def poetx_test_mx4_give_up(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, steps, limit_ns, stream=None) -> int:
+    """Returns the number of blocks of a cluster."""
+    ct, st, bf, _ = _mx4_types or _mx4_setup()
+    dev, n, splits = _device(), d_out * d_in, _I()
+    x = _array(X, "X", n_tokens * (d_out if adjoint else d_in), bf, dev)
+    c = _array(codes, "codes", n // 2, ct, dev)
+    s = _array(scales, "scales", n // POETX_MX4_BLOCK, st, dev)
+    y = _array(Y, "Y", n_tokens * (d_in if adjoint else d_out), bf, dev)
+    _check(lib().poetx_test_mx4_give_up(1 if adjoint else 0, n_tokens, d_in, d_out, x, c, s, y, steps, limit_ns,
+                                        ctypes.byref(splits), _stream(stream, dev)), "poetx_test_mx4_give_up")
+    return splits.value
 
 
 def poetx_test_sqrt(first, last, mismatches, stream=None):

@@ -533,6 +533,9 @@ struct Mx4Args {
   const uint8_t* scales;
   long pitch;            // scales per row of the weight
   __nv_bfloat16* Y;
+  // Give-up probe only (poetx_test_mx4_give_up): steps whose codes the grid's first block copies; the limit of waits.
+  int probe_steps;
+  unsigned long long probe_ns;
 };
 
 // Two groups of eight converter warps, each with every other step, so that one converts while the other waits for
@@ -550,7 +553,11 @@ __host__ __device__ constexpr size_t mx4_smem_bytes(int mh, int tn, int slots, i
   return (size_t)slots * (tn * mx4_bk(mh) * 2 + MX4_W_BYTES) + (size_t)cs * MX4_C_BYTES + 1024 + 512;
 }
 
-template <int MH, bool ADJ>
+// A block that gives up: every role that misses its tile leaves its loop, so that the issuing warp misses one too and
+// commits no accumulators; then all warps' last wait runs out, copies land, and nothing is stored (a cluster stores
+// nothing of a tile that one of its blocks gave up).  PROBE: the same kernel with short limits, whose first block
+// gets no more codes after some steps, so that a test sees this happen.
+template <int MH, bool ADJ, bool PROBE = false>
 __global__ void __launch_bounds__(MX4_THREADS, 1)
     mx4_gemm_tc(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmC, const Mx4Args a) {
   using namespace sm100;
@@ -569,6 +576,10 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   auto cempty = [&](int s) { return sb + 8u * (3 * R + s); }; // code tile read
   const uint32_t accum = sb + 8u * (4 * R);
   uint32_t* holder = reinterpret_cast<uint32_t*>(smem + (sb - sw) + 8 * (4 * R + 1));
+  const uint32_t gave_up = sb + 8u * (4 * R + 2);  // set by a warp that gave up, read by the cluster
+  auto wait = [&](uint32_t bar, uint32_t phase, int site) {
+    return PROBE ? mbar_wait_limit(bar, phase, a.probe_ns, KID_MX4, site) : mbar_wait(bar, phase, KID_MX4, site);
+  };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // Blocks that run together share X tiles and read the whole weight between them.
@@ -588,6 +599,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     fence_mbar_init();
     fence_proxy_async_smem();
   }
+  if (threadIdx.x == 4 * R + 1) st_shared_b32(gave_up, 0u);
   if (warp == MX4_CONV_WARPS + 1 && lane == 0) prefetch_tmap(&tmX);
   if (warp == MX4_CONV_WARPS + 2 && lane == 0) prefetch_tmap(&tmC);
   if (warp == MX4_CONV_WARPS) {
@@ -606,7 +618,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       int t = 0;
       uint32_t phase = 1;
       for (int i = 0; i < nkt; ++i) {
-        if (!mbar_wait(taken(t), phase, KID_MX4, 1)) break;
+        if (!wait(taken(t), phase, 1)) break;
         mbar_arrive_expect_tx(ready(t), x_bytes);
 #pragma unroll
         for (int p = 0; p < KA; ++p)
@@ -620,7 +632,8 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       int s = 0;
       uint32_t phase = 1;
       for (int i = 0; i < nkt; i += CS) {
-        if (!mbar_wait(cempty(s), phase, KID_MX4, 7)) break;
+        if (PROBE && blockIdx.x == 0 && i >= a.probe_steps) break;
+        if (!wait(cempty(s), phase, 7)) break;
         mbar_arrive_expect_tx(cfull(s), C_BYTES);
         const int k0 = (kt0 + i) * BK;
         if (!ADJ) tma_load_2d(sc + s * C_BYTES, &tmC, cfull(s), k0 / 2, m0);
@@ -643,10 +656,10 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     uint32_t w_lo = (uint32_t)wd0, x_lo = (uint32_t)xd0;  // addresses in units of 16 bytes: they never carry
     // The whole warp walks the steps, so that descriptors stay uniform, and one lane issues.
     const bool leader = elect_one();
-    int t = 0;
+    int t = 0, i = 0;
     uint32_t phase = 0;
-    for (int i = 0; i < nkt; ++i) {
-      if (!__all_sync(0xffffffffu, mbar_wait(ready(t), phase, KID_MX4, 2))) break;
+    for (; i < nkt; ++i) {
+      if (!__all_sync(0xffffffffu, wait(ready(t), phase, 2))) break;
       tc_fence_after();
       const uint32_t bar = taken(t), w = w_lo, x = x_lo;
       w_lo += slot_bytes >> 4;
@@ -671,7 +684,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       }
       __syncwarp();
     }
-    if (leader) mma_commit(accum);
+    if (leader && i == nkt) mma_commit(accum);
   } else {
     // ---------------- converters: two blocks of 32 codes (64 columns) of one row per thread and step
     // Forward: rows are features, columns K positions.  Adjoint: rows are K positions, columns features.
@@ -735,9 +748,9 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     for (int i = group; i < nkt; i += CS) {
       const uint32_t scales = next.lo | next.hi << 8;
       next = load_scales();
-      bool ok = mbar_wait(cfull(s), s_phase, KID_MX4, 4);
+      bool ok = wait(cfull(s), s_phase, 4);
       const uint4 c[2] = {ld_shared_v4(sc + s * C_BYTES + c0), ld_shared_v4(sc + s * C_BYTES + c1)};
-      ok = ok && mbar_wait(taken(t), t_phase, KID_MX4, 5);
+      ok = ok && wait(taken(t), t_phase, 5);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const uint32_t tile = sw + t * slot_bytes + dst;  // piece j of the row: position j ^ key of its 128 bytes
@@ -774,10 +787,11 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
   __syncwarp();
 
   // ---------------- epilogue
-  bool ok = mbar_wait(accum, 0, KID_MX4, 6);
+  bool ok = wait(accum, 0, 6);
   ok = __all_sync(0xffffffffu, ok);
   if (!ok) {
-    // Given up: copies still under way land within microseconds; they must find this block's memory.
+    st_shared_b32(gave_up, 1u);
+    // Copies still under way land within microseconds; they must find this block's memory.
     for (const unsigned long long t0 = global_timer_ns(); global_timer_ns() - t0 < 1000000ull;) {
     }
   }
@@ -837,6 +851,8 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       }
       cluster_sync_all();
       if (ok) {
+        uint32_t lost = 0u;
+        for (int r = 0; r < a.splits; ++r) lost |= ld_cluster_u32(mapa_shared(gave_up, (uint32_t)r));
         // Eight features of one token per step: sum over the cluster, round once, 16-byte store.
         for (int e = threadIdx.x; e < share * 16; e += MX4_THREADS) {
           const int c = c_lo + (e >> 4), f = (e & 15) * 8;
@@ -851,6 +867,7 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
 #pragma unroll
               for (int j = 0; j < 8; ++j) x[j] += y[j];
             }
+            if (lost) continue;
             *reinterpret_cast<uint4*>(a.Y + (size_t)n * a.M + m) =
                 make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
           }

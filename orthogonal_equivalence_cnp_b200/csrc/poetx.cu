@@ -570,13 +570,14 @@ Mx4Plan mx4_plan(long M, long N, long K) {
   return p;
 }
 
-template <int MH, bool ADJ>
+// probe_ns: set for the give-up probe alone.
+template <int MH, bool ADJ, bool PROBE = false>
 poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes, const uint8_t* scales, void* Y, int M,
-                        int N, int K, cudaStream_t st, int cls) {
+                        int N, int K, cudaStream_t st, int cls, int probe_steps = 0, unsigned long long probe_ns = 0) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
-  auto kern = mx4_gemm_tc<MH, ADJ>;
+  auto kern = mx4_gemm_tc<MH, ADJ, PROBE>;
   if (!attr_done[dev]) {
     if (!set_smem(kern, 227 * 1024)) return POETX_ERR_CUDA;
     attr_done[dev] = true;
@@ -592,6 +593,7 @@ poetx_status launch_mx4(const Mx4Plan& p, const Operand& X, const Operand& codes
   a.scales = scales;
   a.pitch = codes.cols / 16;
   a.Y = static_cast<__nv_bfloat16*>(Y);
+  a.probe_steps = probe_steps; a.probe_ns = probe_ns;
   cudaLaunchConfig_t cfg = {};
   a.mt = (M + MH * 128 - 1) / (MH * 128);
   const long blocks = (long)a.mt * ((N + p.tn - 1) / p.tn) * p.splits;
@@ -2254,6 +2256,32 @@ poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_st
   LaunchScope ls(POETX_KC_ELEMENTWISE, stream);
   wait_probe_kernel<<<1, 32, 0, stream>>>((unsigned long long)limit_ns, returned);
   return last_launch();
+}
+
+poetx_status poetx_test_mx4_give_up(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
+                                    const uint8_t* scales, void* Y, int steps, long long limit_ns, int* splits,
+                                    poetx_stream stream) {
+  if ((adjoint != 0 && adjoint != 1) || n_tokens <= 0 || steps < 0 || limit_ns < 1000 || limit_ns > 100000000 ||
+      splits == nullptr)
+    return POETX_ERR_INVALID_ARG;
+  POETX_TRY(check_mx4(d_in, d_out));
+  POETX_TRY(check_ptrs({X, codes, scales, Y}));
+  if (X == Y) return POETX_ERR_INVALID_ARG;
+  const int M = adjoint ? d_in : d_out, K = adjoint ? d_out : d_in, n = n_tokens;
+  const Mx4Plan p = mx4_plan(M, n, K);
+  // The first block's share of K must be longer than the steps it gets (whole pairs), or nothing is missed.
+  if ((steps + 1L) / 2 * 2 >= (K + mx4_bk(p.mh) - 1) / mx4_bk(p.mh) / p.splits) return POETX_ERR_INVALID_ARG;
+  *splits = p.splits;
+  const Operand x = view(X, n, K, K), c = view(codes, d_out, d_in / 2, d_in / 2);
+  auto launch = [&](auto mh, auto adj) {
+    return launch_mx4<decltype(mh)::value, decltype(adj)::value, true>(p, x, c, scales, Y, M, n, K, stream,
+                                                                       POETX_KC_TEST_GEMM, steps,
+                                                                       (unsigned long long)limit_ns);
+  };
+  using one = std::integral_constant<int, 1>;
+  using two = std::integral_constant<int, 2>;
+  if (adjoint) return p.mh == 2 ? launch(two(), std::true_type()) : launch(one(), std::true_type());
+  return p.mh == 2 ? launch(two(), std::false_type()) : launch(one(), std::false_type());
 }
 
 __global__ void sqrt_probe_kernel(unsigned first, unsigned last, unsigned long long* mismatches) {

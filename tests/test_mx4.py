@@ -89,3 +89,15 @@ def test_binding_checks_types_and_sizes():
             P.poetx_mx4_quantize(P.POETX_BF16, 4, 64, a["W"], a["codes"], a["scales"], 0)
     with pytest.raises(ValueError, match="Y"):
         P.poetx_mx4_matmul(1, 2, 64, 8, Fake(16, bf), Fake(256, u8), Fake(16, u8), Fake(127, bf), 0)
+
+
+@pytest.mark.parametrize("args,code", [
+    ((0, 64, 512, 512, A, A, A, 2 * A, 0, 999), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 0, 100_000_001), 1),
+    ((0, 64, 512, 512, A, A, A, 2 * A, -1, 1000), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 1 << 30, 1000), 1),
+    ((0, 0, 512, 512, A, A, A, 2 * A, 0, 1000), 1), ((0, 64, 500, 512, A, A, A, 2 * A, 0, 1000), 2),
+    ((0, 64, 512, 512, A, A, A, A, 0, 1000), 1), ((0, 64, 512, 512, A, A + 8, A, 2 * A, 0, 1000), 3),
+])
+def test_give_up_probe_refusals(args, code):
+    splits = ctypes.c_int()
+    assert P.lib().poetx_test_mx4_give_up(*args, ctypes.byref(splits), None) == code
+    assert P.lib().poetx_test_mx4_give_up(0, 64, 512, 512, A, A, A, 2 * A, 0, 1000, None, None) == 1
