@@ -2116,9 +2116,11 @@ poetx_status poetx_xq_merge(const poetx_desc* desc, int8_t* W0q, float* W0s, con
 }
 
 // ------------------------------------------------------------------------------------- MX4
-static poetx_status check_mx4(int d_in, int d_out) {
+static poetx_status check_mx4(int d_in, int d_out, int n_tokens = 0) {
+  // The kernels round each of the three up to a tile, and code tiles run two steps past an end, in 32 bits.
+  constexpr int most = 0x7fffffff - 1024;
   if (d_in <= 0 || d_out <= 0) return POETX_ERR_INVALID_ARG;
-  if (d_in % 32 || d_out % 8) return POETX_ERR_UNSUPPORTED_SHAPE;
+  if (d_in % 32 || d_out % 8 || d_in > most || d_out > most || n_tokens > most) return POETX_ERR_UNSUPPORTED_SHAPE;
   return POETX_OK;
 }
 // The layer on an MX4 weight: as POET-XQ, bf16 and POET-Xmem; any block size (d is a multiple of 64).
@@ -2177,7 +2179,7 @@ poetx_status poetx_mx4_dequantize(int rows, int cols, const uint8_t* codes, cons
 poetx_status poetx_mx4_matmul(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
                               const uint8_t* scales, void* Y, poetx_stream stream) {
   if ((adjoint != 0 && adjoint != 1) || n_tokens < 0) return POETX_ERR_INVALID_ARG;
-  POETX_TRY(check_mx4(d_in, d_out));
+  POETX_TRY(check_mx4(d_in, d_out, n_tokens));
   if (n_tokens == 0) return POETX_OK;
   POETX_TRY(check_ptrs({X, codes, scales, Y}));
   if (X == Y) return POETX_ERR_INVALID_ARG;
@@ -2264,7 +2266,7 @@ poetx_status poetx_test_mx4_give_up(int adjoint, int n_tokens, int d_in, int d_o
   if ((adjoint != 0 && adjoint != 1) || n_tokens <= 0 || steps < 0 || limit_ns < 1000 || limit_ns > 100000000 ||
       splits == nullptr)
     return POETX_ERR_INVALID_ARG;
-  POETX_TRY(check_mx4(d_in, d_out));
+  POETX_TRY(check_mx4(d_in, d_out, n_tokens));
   POETX_TRY(check_ptrs({X, codes, scales, Y}));
   if (X == Y) return POETX_ERR_INVALID_ARG;
   const int M = adjoint ? d_in : d_out, K = adjoint ? d_out : d_in, n = n_tokens;

@@ -101,3 +101,15 @@ def test_give_up_probe_refusals(args, code):
     splits = ctypes.c_int()
     assert P.lib().poetx_test_mx4_give_up(*args, ctypes.byref(splits), None) == code
     assert P.lib().poetx_test_mx4_give_up(0, 64, 512, 512, A, A, A, 2 * A, 0, 1000, None, None) == 1
+
+
+@pytest.mark.parametrize("adjoint", [0, 1])
+def test_sizes_that_a_tile_takes_past_31_bits_are_refused(adjoint):
+    # The first round-up to a tile past 2^31 - 1 would make every loop over K, or the grid, empty: no result, no error.
+    top = 2 ** 31 - 1
+    for n, d_in, d_out in ((1, top // 32 * 32, 8), (1, 32, top // 8 * 8), (top, 32, 8), (1, (top - 1024) // 32 * 32 + 32, 8),
+                           (1, 32, (top - 1024) // 8 * 8 + 8), (top - 1023, 32, 8)):
+        assert P.lib().poetx_mx4_matmul(adjoint, n, d_in, d_out, A, A, A, 2 * A, None) == 2
+    # The largest ones get as far as the pointers.
+    for n, d_in, d_out in ((1, (top - 1024) // 32 * 32, 8), (1, 32, (top - 1024) // 8 * 8), (top - 1024, 32, 8)):
+        assert P.lib().poetx_mx4_matmul(adjoint, n, d_in, d_out, A, A, A, 2 * A + 8, None) == 3
