@@ -110,3 +110,39 @@ def test_mx4_merge_with_zero_theta_is_a_fixed_point():
     Wn, cn, sn, tR, tP = O.mx4_merge(c, s, np.zeros((2, P)), np.zeros((3, P)), pL, pR, pL, pR, b, 3)
     assert np.array_equal(Wn, O.mx4_dequantize(c, s)) and np.array_equal(O.mx4_dequantize(cn, sn), Wn)
     assert not tR.any() and not tP.any()
+
+
+@pytest.mark.parametrize("positive", [False, True])
+@pytest.mark.parametrize("a", [448.0, 447.9, 300.0, 17.3, 1.0, 0.02, 2.0 ** -6, 0.0117, 0.003, 0.0021, 0.0001])
+def test_moments_rounded_stochastically_are_unbiased(positive, a):
+    # Blocks whose first element, 448, makes the scale 1, so that the other 255 stand on the grid as they are; 65536 equidistant
+    # draws over them.  floor(a / g + r / 65536) is up for a fraction of the draws that is a / g's own within one draw,
+    # so the mean is a within 2^-16 of a step (2^-40 of a more for the scale's own division).
+    n = 65536
+    r = np.zeros((258, 256))
+    r[:, 1:] = np.resize(np.arange(n, dtype=float), (258, 255))
+    for sign in ((1.0,) if positive else (1.0, -1.0)):
+        x = np.full((258, 256), sign * a)
+        x[:, 0] = 448.0
+        q, u = O.e4m3_moments(x.ravel(), positive, r.ravel())
+        assert np.array_equal(u, np.ones(258))
+        q = q.reshape(258, 256)
+        assert np.all(q[:, 0] == 448)
+        q = q[:, 1:].ravel()[:n] * sign
+        vals = O.e4m3_values()
+        vals = np.unique(np.abs(vals[np.isfinite(vals)]))
+        lo, hi = vals[vals <= a][-1], vals[vals >= a][0]
+        if positive and lo == 0:  # never stored as zero
+            assert np.all(q == hi) and hi == 2.0 ** -9
+            continue
+        assert set(np.unique(q)) <= {lo, hi}
+        assert abs(q.mean() - a) <= (hi - lo) * 2.0 ** -16 + a * 2.0 ** -40
+        assert a in (lo, hi) or {lo, hi} == set(np.unique(q))  # exact values stay, others go both ways
+
+
+def test_moments_of_zero_stay_zero_under_any_draw():
+    x = np.zeros(256)
+    x[0] = 1.0
+    for positive in (False, True):
+        q, _ = O.e4m3_moments(x, positive, np.full(256, 65535.0))
+        assert q[0] == 448 and not q[1:].any()
