@@ -252,11 +252,12 @@ poetx_status poetx_mx4_dequantize(int rows, int cols, const uint8_t* codes, cons
                                   poetx_stream stream);
 
 /* Product with an MX4 weight W [d_out, d_in]: a merged layer when serving (from one token on), or
- * the frozen part of a training step.
+ * the frozen part of a training step.  The codes of a POET-X layer are those of W0' = Pi_L W0 Pi_R^T: after a merge with
+ * identity permutations the product is the layer; with others it takes X[:, perm_R] and gives Y[:, perm_L].
  *   adjoint = 0:  Y [n, d_out] = X [n, d_in] . W^T        adjoint = 1:  Y [n, d_in] = X [n, d_out] . W
  * X and Y bf16, row-major, not overlapping; sums in float32, rounded once.  d_in a multiple of 32, d_out of 8, all
- * three under 2^31 - 1024 (UNSUPPORTED_SHAPE otherwise).  n_tokens == 0 launches nothing.  The same arguments give the same bits; the order of
- * a token's sums, and so its last bits, may change with n_tokens. */
+ * three under 2^31 - 1024 (UNSUPPORTED_SHAPE otherwise).  n_tokens == 0 launches nothing.  The same
+ * arguments give the same bits; the order of a token's sums, and so its last bits, may change with n_tokens. */
 poetx_status poetx_mx4_matmul(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
                               const uint8_t* scales, void* Y, poetx_stream stream);
 
