@@ -40,6 +40,7 @@ class PoetxLayer:
         # (after quantize("mx4")): 4-bit codes W0q uint8 [d_out, d_in / 2], scales W0s uint8 [d_out, d_in / 32].
         self.xq = self.mx4 = False
         self.W0q = self.W0s = None
+        self.W0 = None  # the un-absorbed weight (load_state), for the four-permutation comparator
         # theta_R and theta_P (and their gradients and AdamW moments) are stored back to back so
         # that one optimiser launch covers both sides.
         nbo, nbi = dout // b, din // b
@@ -75,7 +76,7 @@ class PoetxLayer:
         self.theta_P.copy_(torch.from_numpy(np.asarray(theta_P, np.float32)))
         W0_dev = self.to_dev(W0)
         poetx_absorb(self.desc, W0_dev, self.perm_L, self.perm_R, self.W0p)
-        self.W0 = W0_dev  # the un-absorbed weight, kept for the four-permutation comparator
+        self.W0 = W0_dev
 
     # ------------------------------------------------------------------------- the step
     def cnp(self):
@@ -106,8 +107,9 @@ class PoetxLayer:
         return self.dX, self.g_R, self.g_P
 
     def quantize(self, bits: str = "int8"):
-        """Switches the layer (mem mode, bf16) to a quantised W0' and releases the bf16 one: "int8"
-        (POET-XQ, one scale per row) or "mx4" (4 bits, one scale per 32 columns)."""
+        """Switches the layer (mem mode, bf16) to a quantised W0' and releases the bf16 one and the
+        un-absorbed W0 (the four-permutation comparator ends with it): "int8" (POET-XQ, one scale per row)
+        or "mx4" (4 bits, one scale per 32 columns)."""
         if bits not in ("int8", "mx4"):
             raise ValueError(f"bits: 'int8' or 'mx4', got {bits!r}")
         if self.xq or self.mx4:
@@ -126,7 +128,7 @@ class PoetxLayer:
             poetx_xq_quantize(d, self.W0p, W0q, W0s)
             self.xq = True
         self.W0q, self.W0s = W0q, W0s
-        self.W0p = None  # stream-ordered release: the quantiser has been enqueued before it
+        self.W0p = self.W0 = None  # stream-ordered release: the quantiser has been enqueued before it
 
     def cnp_forward(self, X: torch.Tensor):
         """CNP and layer forward in one library call (the CNP overlaps the input gather)."""
@@ -173,6 +175,9 @@ class PoetxLayer:
     def fourperm_step(self, X: torch.Tensor, dY: torch.Tensor):
         """The same step with none of the permutations absorbed (comparator): R and P applied around
         the original W0, four activation permutations per pass.  Same outputs as step()."""
+        if self.W0 is None:
+            raise ValueError("the four-permutation comparator needs the un-absorbed weight: load_state() keeps it, "
+                             "quantize() releases it")
         if getattr(self, "fp_saved", None) is None:
             self.fp_saved = torch.empty(self.n * (self.desc.d_in + self.desc.d_out), dtype=self.dtype,
                                         device=self.device)

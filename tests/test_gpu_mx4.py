@@ -595,3 +595,19 @@ def test_refusals_and_empty_calls():
     with pytest.raises(ValueError, match="contiguous"):
         P.poetx_mx4_matmul(0, 4, 512, 512, torch.empty(8, 512, dtype=torch.bfloat16, device="cuda")[::2], L.W0q, L.W0s, L.Y)
     device_clean()
+
+
+@pytest.mark.parametrize("bits", ["mx4", "int8"])
+def test_quantize_releases_every_bf16_weight(bits):
+    d = 2048
+    held = lambda: torch.cuda.memory_stats()["requested_bytes.all.current"]  # without the allocator's own rounding
+    inp = I.make_layer(I.small_shape(d, d, 256, 3, 8, "bf16", "mem", theta_std=0.005, w_std=0.02), 3, with_activations=False)
+    L = PoetxLayer(make_desc(d, d, 256, 3, "bf16", "mem"), 8)
+    before = held() - 2 * d * d  # without W0'
+    L.load_state(inp.W0, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R)
+    L.quantize(bits)
+    assert held() - before == (d * d // 2 + d * d // 32 if bits == "mx4" else d * d + 4 * d)  # codes and scales
+    assert L.W0 is None and L.W0p is None
+    with pytest.raises(ValueError, match="un-absorbed"):
+        L.fourperm_step(L.dX, L.Y)
+    device_clean()
