@@ -70,6 +70,8 @@ class PoetxLayer:
 
     def load_state(self, W0: np.ndarray, theta_R, theta_P, pi_L, pi_R):
         """Uploads the original-basis W0 and absorbs the two permutations on the device."""
+        if self.W0p is None:
+            raise ValueError("the layer's weight is quantised; load the state into a new layer")
         self.perm_L.copy_(torch.from_numpy(np.asarray(pi_L, np.int32)))
         self.perm_R.copy_(torch.from_numpy(np.asarray(pi_R, np.int32)))
         self.theta_R.copy_(torch.from_numpy(np.asarray(theta_R, np.float32)))

@@ -14,3 +14,14 @@ def test_four_permutation_comparator_needs_the_weight_that_quantize_releases():
     L = _layer()
     with pytest.raises(ValueError, match="un-absorbed"):
         L.fourperm_step(L.dX, L.Y)
+
+
+def test_a_quantised_layer_takes_no_new_state():
+    # Refused before anything is overwritten.
+    L = _layer()
+    L.mx4, L.W0p = True, None  # as quantize() leaves it
+    n, k = 512 // 64, 256 // 64
+    with pytest.raises(ValueError, match="quantised"):
+        L.load_state(torch.zeros(512, 256).numpy(), torch.ones(n, 2016).numpy(), torch.ones(k, 2016).numpy(),
+                     torch.arange(511, -1, -1).numpy(), torch.arange(255, -1, -1).numpy())
+    assert not L.theta.any() and torch.equal(L.perm_L, torch.arange(512, dtype=torch.int32))
