@@ -42,7 +42,9 @@ def new_moments(param: torch.Tensor, moments: str = "e4m3"):
 
 class MultiAdamW:
     """The tensors of one optimiser on one device.  Keeps references to them; their addresses must
-    not change while it is used (gradients are written in place, as the layers and GradBuckets do)."""
+    not change while it is used (gradients are written in place, as the layers and GradBuckets do).
+    All of them share one step count: tensors whose moments restart at different times (theta, which a
+    merge restarts, and norms or embeddings, which it does not) take an object each."""
 
     def __init__(self, tensors):
         self.tensors = [x if isinstance(x, AdamWTensor) else AdamWTensor(*x) for x in tensors]
@@ -112,10 +114,15 @@ class MultiAdamW:
             poetx_adamw_multi_step(cfg, len(self.tensors), self._entries, t, seed, stream)
         self.t = t
 
-    def reset(self):
-        """Zeroes the moments, as after a merge; the step count starts again."""
-        for x in self.tensors:
-            for a in (x.m, x.v, x.scale):
-                if a is not None:
-                    (a.view(torch.uint8) if a.dtype == torch.float8_e4m3fn else a).zero_()
+    def reset(self, stream=None):
+        """Zeroes the moments, as after a merge, in the order of `stream` (as step takes it); the step count
+        starts again."""
+        if self._device is not None:
+            if isinstance(stream, int):
+                stream = torch.cuda.ExternalStream(stream, self._device)
+            with torch.cuda.device(self._device), torch.cuda.stream(stream):
+                for x in self.tensors:
+                    for a in (x.m, x.v, x.scale):
+                        if a is not None:
+                            (a.view(torch.uint8) if a.dtype == torch.float8_e4m3fn else a).zero_()
         self.t = 0

@@ -298,3 +298,31 @@ def test_square_root_of_every_float():
     bad = torch.ones(1, dtype=torch.int64, device="cuda")
     P.poetx_test_sqrt(0x0D800000, 0x7F7FFFFF, bad)
     assert int(bad) == 0
+
+
+@pytest.mark.parametrize("how", ["stream", "handle", "capture"])
+def test_reset_is_ordered_on_the_stream_of_the_step(how):
+    # A step held back on another stream, then a reset given the same stream: the reset comes after the step.
+    xs = [_make(np.random.default_rng(i), 3000 + i, "e4m3" if i else "f32", torch.float32, torch.float32) for i in range(2)]
+    before = [x.param.clone() for x in xs]
+    opt = MultiAdamW(xs)
+    st = torch.cuda.Stream()
+    arg = st.cuda_stream if how == "handle" else st
+    torch.cuda.synchronize()
+    if how == "capture":
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=st):
+            opt.step(_cfg(), t=4, seed=1, stream=arg)
+            opt.reset(stream=arg)
+        graph.replay()
+    else:
+        with torch.cuda.stream(st):
+            torch.cuda._sleep(100_000_000)  # about 50 ms
+        opt.step(_cfg(), t=4, seed=1, stream=arg)
+        opt.reset(stream=arg)
+    torch.cuda.synchronize()
+    assert opt.t == 0
+    for x, p in zip(xs, before):
+        assert not torch.equal(x.param, p)
+        assert not any(a.view(torch.uint8).any().item() for a in (x.m, x.v))
+        assert x.scale is None or not x.scale.any().item()
