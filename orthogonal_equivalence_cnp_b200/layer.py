@@ -14,6 +14,7 @@ from . import (POETX_BF16, POETX_F32, POETX_FAST, POETX_MEM, poetx_absorb, poetx
                poetx_merge, poetx_mx4_backward, poetx_mx4_forward, poetx_mx4_merge, poetx_mx4_quantize,
                poetx_wc_backward, poetx_wc_forward, poetx_wc_saved_size, poetx_wc_workspace_size,
                poetx_workspace_size, poetx_xq_backward, poetx_xq_forward, poetx_xq_merge, poetx_xq_quantize)
+from .optim import MultiAdamW
 
 TORCH_DTYPE = {POETX_F32: torch.float32, POETX_BF16: torch.bfloat16}
 
@@ -24,9 +25,13 @@ def make_desc(d_in: int, d_out: int, b: int, k: int, dtype: str, mode: str) -> p
 
 
 class PoetxLayer:
-    """Holds W0', theta, permutations, Q and scratch of one layer on one device."""
+    """Holds W0', theta, permutations, Q and scratch of one layer on one device.  moments: the AdamW moments that
+    optimizer_step and train_step use, "f32" (m and v), "e4m3" (8 bits each, in `optimizer`), or None where theta is
+    stepped from outside, by a MultiAdamW over several layers."""
 
-    def __init__(self, desc: poetx_desc, n_tokens: int, device="cuda"):
+    def __init__(self, desc: poetx_desc, n_tokens: int, device="cuda", moments="f32"):
+        if moments not in ("f32", "e4m3", None):
+            raise ValueError(f"moments: 'f32', 'e4m3' or None, got {moments!r}")
         self.desc = desc
         self.n = int(n_tokens)
         self.device = torch.device(device)
@@ -56,8 +61,11 @@ class PoetxLayer:
         self.dX = torch.empty(self.n, din, dtype=dt, device=dev)
         self.grad = torch.zeros_like(self.theta)
         self.g_R, self.g_P = self.grad[:nbo], self.grad[nbo:]
-        self.m = torch.zeros_like(self.theta)
-        self.v = torch.zeros_like(self.theta)
+        self.m = self.v = self.optimizer = None
+        if moments == "f32":
+            self.m, self.v = torch.zeros_like(self.theta), torch.zeros_like(self.theta)
+        elif moments == "e4m3":
+            self.optimizer = MultiAdamW.from_params([self.theta], [self.grad])
         self.t = 0       # AdamW step count of the current moments
         self.steps = 0   # training steps taken (drives the merge schedule)
         ws = poetx_workspace_size(desc, self.n)
@@ -151,18 +159,27 @@ class PoetxLayer:
         if grad_ready is not None:
             grad_ready()
 
-    def optimizer_step(self, cfg: poetx_adamw_cfg):
-        """AdamW on the packed theta (both sides in one launch)."""
+    def optimizer_step(self, cfg: poetx_adamw_cfg, seed: int = 0):
+        """AdamW on the packed theta (both sides in one launch).  seed: of the 8-bit moments' rounding (0: to
+        nearest; another each step: stochastic)."""
+        if self.optimizer is not None:
+            x = self.optimizer.tensors[0]
+            if x.param is not self.theta or x.grad is not self.grad:  # moved, as into a flat gradient buffer
+                self.optimizer = MultiAdamW([x._replace(param=self.theta, grad=self.grad)])
+            self.optimizer.step(cfg, t=self.t + 1, seed=seed)
+        elif self.m is not None:
+            poetx_adamw_step(cfg, self.theta.numel(), self.t + 1, self.theta, self.grad, self.m, self.v)
+        else:
+            raise ValueError("the layer holds no moments (moments=None): step theta from outside")
         self.t += 1
-        poetx_adamw_step(cfg, self.theta.numel(), self.t, self.theta, self.grad, self.m, self.v)
 
     def train_step(self, X: torch.Tensor, dY: torch.Tensor, cfg: poetx_adamw_cfg, reset_gap: int = 400,
-                   new_perms=None):
-        """One training step with the merge schedule: CNP, forward, backward, AdamW; after every
-        reset_gap steps merge-then-reinitialise with the permutations new_perms() returns
-        (host int32 arrays pi_L, pi_R) and restart the moments."""
+                   new_perms=None, seed: int = 0):
+        """One training step with the merge schedule: CNP, forward, backward, AdamW (seed: as
+        optimizer_step's); after every reset_gap steps merge-then-reinitialise with the permutations
+        new_perms() returns (host int32 arrays pi_L, pi_R) and restart the moments."""
         self.step(X, dY)
-        self.optimizer_step(cfg)
+        self.optimizer_step(cfg, seed)
         self.steps += 1
         if reset_gap and self.steps % reset_gap == 0:
             if new_perms is None:
@@ -171,7 +188,10 @@ class PoetxLayer:
             self.cnp()  # Q of the theta being folded in
             self.merge(torch.from_numpy(np.asarray(pL, np.int32)).to(self.device),
                        torch.from_numpy(np.asarray(pR, np.int32)).to(self.device))
-            poetx_adamw_reset(self.m.numel(), self.m, self.v)
+            if self.optimizer is not None:
+                self.optimizer.reset()
+            else:
+                poetx_adamw_reset(self.m.numel(), self.m, self.v)
             self.t = 0
 
     def fourperm_step(self, X: torch.Tensor, dY: torch.Tensor):

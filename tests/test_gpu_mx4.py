@@ -611,3 +611,59 @@ def test_quantize_releases_every_bf16_weight(bits):
     with pytest.raises(ValueError, match="un-absorbed"):
         L.fourperm_step(L.dX, L.Y)
     device_clean()
+
+
+def test_moments_held_by_a_layer():
+    desc = make_desc(2048, 2048, 256, 3, "bf16", "mem")
+    held = lambda: torch.cuda.memory_stats()["requested_bytes.all.current"]
+    sizes = {}
+    for moments in ("f32", "e4m3", None):
+        before = held()
+        L = PoetxLayer(desc, 8, moments=moments)
+        sizes[moments] = held() - before
+        n = L.theta.numel()
+        del L
+    assert sizes["f32"] - sizes[None] == 8 * n and sizes["e4m3"] - sizes[None] == 2 * n + 8 * (n // 256)
+
+
+@pytest.mark.parametrize("bits", ["mx4", "int8", None])
+def test_train_step_with_8_bit_moments_and_merges(bits):
+    # The layer's own schedule against the same calls made one by one with an optimiser from outside: the same bits.
+    s = I.small_shape(512, 768, 256, 3, 64, "bf16", "mem", theta_std=0.005, w_std=0.02)
+    inp = I.make_layer(s, 71)
+    cfg = P.poetx_adamw_cfg(1e-3, 0.5, 0.9, 0.999, 1e-8, 0.01)
+    perms = [I.fresh_permutations(s, 300 + i) for i in range(2)]
+    layers = []
+    for moments in ("e4m3", None):
+        L = PoetxLayer(make_desc(512, 768, 256, 3, "bf16", "mem"), 64, moments=moments)
+        L.load_state(inp.W0, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R)
+        if bits:
+            L.quantize(bits)
+        layers.append(L)
+    A, B = layers
+    X, dY = A.to_dev(inp.X), A.to_dev(inp.dY)
+    queue = list(perms)
+    for i in range(5):
+        A.train_step(X, dY, cfg, reset_gap=2, new_perms=lambda: queue.pop(0), seed=i + 1)
+        if i == 2:  # gradients moved into a buffer of several layers
+            flat = torch.zeros(A.grad.numel() + 256, device="cuda")
+            nbo = A.g_R.shape[0]
+            A.grad = flat[256:].view(A.grad.shape)
+            A.g_R, A.g_P = A.grad[:nbo], A.grad[nbo:]
+    assert not queue and A.t == 1 and A.steps == 5
+    opt = MultiAdamW.from_params([B.theta], [B.grad])
+    for i in range(5):
+        B.step(X, dY)
+        opt.step(cfg, seed=i + 1)
+        if i in (1, 3):
+            B.cnp()
+            B.merge(*(torch.from_numpy(p).cuda() for p in perms[i // 2]))
+            opt.reset()
+    torch.cuda.synchronize()
+    device_clean()
+    assert torch.equal(A.theta, B.theta) and A.theta.any().item()
+    assert torch.equal(A.perm_L, B.perm_L) and torch.equal(A.perm_R, B.perm_R)
+    for a, b in ((A.W0q, B.W0q), (A.W0s, B.W0s)) if bits else ((A.W0p, B.W0p),):
+        assert torch.equal(a, b)
+    x, y = A.optimizer.tensors[0], opt.tensors[0]
+    assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in ((x.m, y.m), (x.v, y.v), (x.scale, y.scale)))

@@ -25,3 +25,15 @@ def test_a_quantised_layer_takes_no_new_state():
         L.load_state(torch.zeros(512, 256).numpy(), torch.ones(n, 2016).numpy(), torch.ones(k, 2016).numpy(),
                      torch.arange(511, -1, -1).numpy(), torch.arange(255, -1, -1).numpy())
     assert not L.theta.any() and torch.equal(L.perm_L, torch.arange(512, dtype=torch.int32))
+
+
+def test_moments_of_a_layer():
+    with pytest.raises(ValueError, match="moments"):
+        _layer(moments="int8")
+    L = _layer()
+    assert L.m.shape == L.theta.shape and L.v.shape == L.theta.shape and L.optimizer is None
+    L = _layer(moments=None)
+    assert L.m is None and L.v is None and L.optimizer is None
+    with pytest.raises(ValueError, match="no moments"):
+        L.optimizer_step(P.poetx_adamw_cfg(1e-4, 0.5, 0.9, 0.999, 1e-8, 0.0))
+    assert L.t == 0
