@@ -27,9 +27,11 @@ def make_desc(d_in: int, d_out: int, b: int, k: int, dtype: str, mode: str) -> p
 class PoetxLayer:
     """Holds W0', theta, permutations, Q and scratch of one layer on one device.  moments: the AdamW moments that
     optimizer_step and train_step use, "f32" (m and v), "e4m3" (8 bits each, in `optimizer`), or None where theta is
-    stepped from outside, by a MultiAdamW over several layers."""
+    stepped from outside, by a MultiAdamW over several layers.  workspace: scratch to use instead of the layer's own, a
+    uint8 tensor of at least workspace_bytes(desc, n_tokens); layers that run one after another on one stream
+    may share one (its merge part alone is two bf16 weights)."""
 
-    def __init__(self, desc: poetx_desc, n_tokens: int, device="cuda", moments="f32"):
+    def __init__(self, desc: poetx_desc, n_tokens: int, device="cuda", moments="f32", workspace=None):
         if moments not in ("f32", "e4m3", None):
             raise ValueError(f"moments: 'f32', 'e4m3' or None, got {moments!r}")
         self.desc = desc
@@ -68,8 +70,16 @@ class PoetxLayer:
             self.optimizer = MultiAdamW.from_params([self.theta], [self.grad])
         self.t = 0       # AdamW step count of the current moments
         self.steps = 0   # training steps taken (drives the merge schedule)
-        ws = poetx_workspace_size(desc, self.n)
-        self.ws = torch.empty(max(ws, 256), dtype=torch.uint8, device=dev)
+        ws = self.workspace_bytes(desc, self.n)
+        self.ws = torch.empty(ws, dtype=torch.uint8, device=dev) if workspace is None else workspace
+        if self.ws.dtype != torch.uint8 or not self.ws.is_contiguous() or self.ws.numel() < ws:
+            raise ValueError(f"workspace: a contiguous uint8 tensor of at least {ws} bytes")
+        if self.ws.device != self.theta.device:
+            raise ValueError(f"workspace is on {self.ws.device}, the layer on {self.theta.device}")
+
+    @staticmethod
+    def workspace_bytes(desc: poetx_desc, n_tokens: int) -> int:
+        return max(poetx_workspace_size(desc, n_tokens), 256)
 
     # ------------------------------------------------------------------ state upload helpers
     def to_dev(self, a: np.ndarray, dtype=None) -> torch.Tensor:

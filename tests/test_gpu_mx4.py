@@ -667,3 +667,40 @@ def test_train_step_with_8_bit_moments_and_merges(bits):
         assert torch.equal(a, b)
     x, y = A.optimizer.tensors[0], opt.tensors[0]
     assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in ((x.m, y.m), (x.v, y.v), (x.scale, y.scale)))
+
+
+def test_layers_that_share_a_workspace():
+    # Two layers of different sizes, steps and merges in turn: the same bits as with a workspace each, and what a
+    # layer on MX4 with 8-bit moments and shared scratch holds is its codes, theta, gradient, moments and activations.
+    shapes = [I.small_shape(512, 768, 256, 3, 64, "bf16", "mem", theta_std=0.005, w_std=0.02),
+              I.small_shape(1024, 512, 128, 3, 96, "bf16", "mem", theta_std=0.005, w_std=0.02)]
+    inps = [I.make_layer(s, 80 + i) for i, s in enumerate(shapes)]
+    descs = [make_desc(s.d_in, s.d_out, s.b, 3, "bf16", "mem") for s in shapes]
+    ws = torch.empty(max(PoetxLayer.workspace_bytes(d, s.n_tokens) for d, s in zip(descs, shapes)), dtype=torch.uint8,
+                     device="cuda")
+    cfg = P.poetx_adamw_cfg(1e-3, 0.5, 0.9, 0.999, 1e-8, 0.01)
+    runs = []
+    for shared in (None, ws):
+        layers = []
+        for inp, d, s in zip(inps, descs, shapes):
+            before = torch.cuda.memory_stats()["requested_bytes.all.current"]
+            L = PoetxLayer(d, s.n_tokens, moments="e4m3", workspace=shared)
+            L.load_state(inp.W0, inp.theta_R, inp.theta_P, inp.pi_L, inp.pi_R)
+            L.quantize("mx4")
+            layers.append(L)
+            if shared is not None:
+                torch.cuda.synchronize()
+                n, side = L.theta.numel(), d.d_in + d.d_out
+                assert torch.cuda.memory_stats()["requested_bytes.all.current"] - before == (
+                    d.d_in * d.d_out * 17 // 32 + 8 * n + 2 * n + 8 * ((n + 255) // 256) + 2 * s.n_tokens * side
+                    + 2 * d.b * side + 4 * side)
+        acts = [(L.to_dev(inp.X), L.to_dev(inp.dY)) for L, inp in zip(layers, inps)]
+        for step in range(4):
+            for i, (L, (X, dY)) in enumerate(zip(layers, acts)):
+                L.train_step(X, dY, cfg, reset_gap=2, seed=step + 1,
+                             new_perms=lambda: I.fresh_permutations(shapes[i], 500 + 10 * i + step))
+        torch.cuda.synchronize()
+        runs.append([t.clone() for L in layers for t in (L.theta, L.Y, L.dX, L.grad, L.W0q, L.W0s)])
+        del layers, L
+    device_clean()
+    assert all(torch.equal(a, b) for a, b in zip(*runs))

@@ -37,3 +37,16 @@ def test_moments_of_a_layer():
     with pytest.raises(ValueError, match="no moments"):
         L.optimizer_step(P.poetx_adamw_cfg(1e-4, 0.5, 0.9, 0.999, 1e-8, 0.0))
     assert L.t == 0
+
+
+def test_workspace_from_outside():
+    d = make_desc(256, 512, 64, 3, "bf16", "mem")
+    need = PoetxLayer.workspace_bytes(d, 8)
+    assert need == max(P.poetx_workspace_size(d, 8), 256) and _layer().ws.numel() == need
+    ws = torch.empty(need + 64, dtype=torch.uint8)
+    assert _layer(workspace=ws).ws is ws
+    for bad in (torch.empty(need - 1, dtype=torch.uint8), torch.empty(need), torch.empty(2 * need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            _layer(workspace=bad)
+    with pytest.raises(ValueError, match="is on"):
+        _layer(workspace=torch.empty(need, dtype=torch.uint8, device="meta"))
