@@ -220,8 +220,13 @@ def _nbytes(x):
 def _stream(s, device=None):
     if s is None:
         # The raw handle of the current stream: building torch's Stream object for it costs 3 us, more than a launch.
+        # That call is not part of torch's public interface, so a torch without it takes the object.
         torch = _torch_module or _torch()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if device is None else device)
+        device = torch.cuda.current_device() if device is None else device
+        try:
+            return torch._C._cuda_getCurrentRawStream(device)
+        except AttributeError:
+            return torch.cuda.current_stream(device).cuda_stream
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -413,18 +418,24 @@ _mx4_types = None
 
 
 def _mx4_setup():
-    """Types of codes and scales (two weights a byte and E8M0, as uint8 or under torch's own names) and of values."""
+    """Types of codes and scales (two weights a byte and E8M0, as uint8 or under torch's own names, where this torch
+    has them) and of values."""
     global _mx4_types
     torch = _torch()
-    _mx4_types = ((torch.uint8, torch.float4_e2m1fn_x2), (torch.uint8, torch.float8_e8m0fnu),
-                  (torch.bfloat16,), (torch.float32,))
+    own = lambda name: (torch.uint8, getattr(torch, name)) if hasattr(torch, name) else (torch.uint8,)
+    _mx4_types = (own("float4_e2m1fn_x2"), own("float8_e8m0fnu"), (torch.bfloat16,), (torch.float32,))
     return _mx4_types
 
 
 def _device():
     """The current CUDA device, without initialising CUDA for it."""
     torch = _torch_module or _torch()
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else 0
+    if not torch.cuda.is_initialized():
+        return 0
+    try:
+        return torch._C._cuda_getDevice()  # current_device() without its own check
+    except AttributeError:
+        return torch.cuda.current_device()
 
 
 def _mx4(rows, cols, codes, scales):

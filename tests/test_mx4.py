@@ -113,3 +113,18 @@ def test_sizes_that_a_tile_takes_past_31_bits_are_refused(adjoint):
     # The largest ones get as far as the pointers.
     for n, d_in, d_out in ((1, (top - 1024) // 32 * 32, 8), (1, 32, (top - 1024) // 8 * 8), (top - 1024, 32, 8)):
         assert P.lib().poetx_mx4_matmul(adjoint, n, d_in, d_out, A, A, A, 2 * A + 8, None) == 3
+
+
+def test_a_torch_without_the_newer_names(monkeypatch):
+    # Neither the 4-bit and E8M0 types nor the raw handles: the calls fall back on uint8 and the public interface.
+    from types import SimpleNamespace
+    old = SimpleNamespace(uint8=torch.uint8, bfloat16=torch.bfloat16, float32=torch.float32, _C=SimpleNamespace(),
+                          cuda=SimpleNamespace(is_initialized=lambda: True, current_device=lambda: 3,
+                                               current_stream=lambda d: SimpleNamespace(cuda_stream=1000 + d)))
+    monkeypatch.setattr(P, "_torch_module", old)
+    monkeypatch.setattr(P, "_mx4_types", None)
+    assert P._device() == 3 and P._stream(None) == 1003 and P._stream(None, 2) == 1002
+    assert P._mx4_setup() == ((torch.uint8,), (torch.uint8,), (torch.bfloat16,), (torch.float32,))
+    new = SimpleNamespace(**vars(old), float4_e2m1fn_x2="f4", float8_e8m0fnu="e8")
+    monkeypatch.setattr(P, "_torch_module", new)
+    assert P._mx4_setup()[:2] == ((torch.uint8, "f4"), (torch.uint8, "e8"))
