@@ -389,12 +389,12 @@ def xq_merge(q, s, theta_R, theta_P, pi_L, pi_R, pi_L_new, pi_R_new, b, k):
 # 256 consecutive elements of a tensor share u = max|x| / 448 (x: the first moment, or the root of
 # the second), and each holds x / u on the e4m3 grid: 3 mantissa bits from 2^-6 to 448, multiples of
 # 2^-9 below.  Rounding is to nearest (ties to even), or up with the probability of the part cut off.
-def element_bits(n, tensor, seed):
-    """32 random bits of elements 0..n-1 of the tensor at position `tensor`: two rounds of
+def element_bits(n, tensor, seed, start=0):
+    """32 random bits of elements start..start + n - 1 of the tensor at position `tensor`: two rounds of
     multiply and xor-shift, in integers modulo 2^32."""
     M = 0xFFFFFFFF
     salt = ((seed & M) + ((seed >> 32) & M) * 0x3C6EF373 + (tensor + 1) * 0xBB67AE85) & M
-    i = np.arange(n, dtype=np.uint64)
+    i = np.arange(start, start + n, dtype=np.uint64)
     m32 = np.uint64(M)
     h = ((i & m32) * np.uint64(0x9E3779B1) + np.uint64(salt) + (i >> np.uint64(32)) * np.uint64(0x6A09E667)) & m32
     h = ((h ^ (h >> np.uint64(16))) * np.uint64(0x6A09E667)) & m32

@@ -326,3 +326,27 @@ def test_reset_is_ordered_on_the_stream_of_the_step(how):
         assert not torch.equal(x.param, p)
         assert not any(a.view(torch.uint8).any().item() for a in (x.m, x.v))
         assert x.scale is None or not x.scale.any().item()
+
+
+@pytest.mark.parametrize("seed", [0, 9])
+def test_elements_past_32_bits(seed, monkeypatch):
+    # A tensor of 2^32 + 1029 elements, zeros but for its last 1285, which start 256 before element 2^32: values and
+    # random bits are those of these positions, and the zeros stay.
+    n, at = (1 << 32) + 1029, (1 << 32) - 256
+    tail = _make(np.random.default_rng(17), n - at, "e4m3", torch.bfloat16, torch.bfloat16)
+    zeros = lambda dtype: torch.zeros(n, dtype=dtype, device="cuda")
+    m, v = zeros(torch.uint8), zeros(torch.uint8)
+    big = AdamWTensor(zeros(torch.bfloat16), zeros(torch.bfloat16), m.view(torch.float8_e4m3fn), v.view(torch.float8_e4m3fn),
+                      torch.zeros((n + 255) // 256, 2, device="cuda"))
+    cut = AdamWTensor(*(a[at:] for a in big[:4]), big.scale[at // 256:])
+    for a, b in zip(cut[:5], tail[:5]):
+        a.view(torch.uint8).copy_(b.view(torch.uint8))
+    bits = O.element_bits
+    monkeypatch.setattr(O, "element_bits", lambda count, tensor, s: bits(count, tensor, s, start=at))
+    expect = _expect(tail, 0, 5, seed)
+    MultiAdamW([big]).step(_cfg(), t=5, seed=seed)
+    torch.cuda.synchronize()
+    device_clean()
+    _check(cut, expect, seed)
+    for a in (big.param[:at], m[:at], v[:at], big.scale[:at // 256]):
+        assert not a.view(torch.int64).any().item()

@@ -146,3 +146,17 @@ def test_moments_of_zero_stay_zero_under_any_draw():
     for positive in (False, True):
         q, _ = O.e4m3_moments(x, positive, np.full(256, 65535.0))
         assert q[0] == 448 and not q[1:].any()
+
+
+def test_element_bits_go_on_past_32_bits():
+    # One formula for every position: a later start continues the sequence, and past 2^32 it does not repeat.
+    a = O.element_bits(1000, 2, 77)
+    assert np.array_equal(O.element_bits(600, 2, 77, start=400), a[400:])
+    far = O.element_bits(1000, 2, 77, start=(1 << 32) - 500)
+    assert not np.array_equal(far[500:], a[:500])
+    # By hand: element 2^32 + 1 of tensor 0 under seed 0 (salt 0xBB67AE85).
+    M = 0xFFFFFFFF
+    h = (0x9E3779B1 + 0xBB67AE85 + 0x6A09E667) & M
+    h = ((h ^ (h >> 16)) * 0x6A09E667) & M
+    h = ((h ^ (h >> 15)) * 0xBB67AE85) & M
+    assert int(O.element_bits(1, 0, 0, start=(1 << 32) + 1)[0]) == h ^ (h >> 16)
