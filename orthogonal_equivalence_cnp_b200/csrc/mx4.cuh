@@ -109,25 +109,24 @@ __global__ void __launch_bounds__(256) mx4_quantize_kernel(const uint4* __restri
                                                            uint32_t* __restrict__ codes, uint8_t* __restrict__ scales) {
   sm100::griddep_wait();
   constexpr int U = BF ? MX4_AT_ONCE : MX4_AT_ONCE / 2, V = BF ? 1 : 2;  // 16-byte loads per chunk: V
-  // Chunks and strides are multiples of 4: the shuffles' partners are all here or none is.
+  // Batches while the whole warp has one; then piece by piece, where a warp may end in the middle: chunks and strides
+  // are multiples of 4, so the four threads of a scale go together, and their shuffles name them alone.
   const long stride = (long)gridDim.x * blockDim.x;
   long i = (long)blockIdx.x * blockDim.x + threadIdx.x;
-  for (; i + (U - 1) * stride < chunks; i += U * stride) {
-    const uint32_t mask = __activemask();
+  for (; (i | 31) + (U - 1) * stride < chunks; i += U * stride) {
     uint4 in[U][2] = {};
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
       for (int v = 0; v < V; ++v) in[u][v] = W[(i + u * stride) * V + v];
 #pragma unroll
-    for (int u = 0; u < U; ++u) mx4_quantize8<BF>(in[u], i + u * stride, mask, codes, scales);
+    for (int u = 0; u < U; ++u) mx4_quantize8<BF>(in[u], i + u * stride, 0xffffffffu, codes, scales);
   }
   for (; i < chunks; i += stride) {
-    const uint32_t mask = __activemask();
     uint4 in[2] = {};
 #pragma unroll
     for (int v = 0; v < V; ++v) in[v] = W[i * V + v];
-    mx4_quantize8<BF>(in, i, mask, codes, scales);
+    mx4_quantize8<BF>(in, i, 0xFu << (threadIdx.x & 28), codes, scales);
   }
 }
 

@@ -704,3 +704,20 @@ def test_layers_that_share_a_workspace():
         del layers, L
     device_clean()
     assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,cols", [(1187, 2080), (2411, 1056)])
+def test_quantize_batches_that_end_inside_a_warp(dtype, rows, cols):
+    # More pieces of eight than there are resident threads, and no whole number of warps of them.
+    assert rows * cols // 8 > 256 * 8 * 148 and rows * cols // 8 % 32
+    W = _special(rows, cols, dtype, rows)
+    t = torch.from_numpy(W).cuda().to(torch.bfloat16 if dtype == "bf16" else torch.float32)
+    codes, scales = _empty(rows, cols)
+    P.poetx_mx4_quantize(P.POETX_BF16 if dtype == "bf16" else P.POETX_F32, rows, cols, t, codes, scales)
+    back = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    P.poetx_mx4_dequantize(rows, cols, codes, scales, back)
+    c, s = O.mx4_quantize(W)
+    assert np.array_equal(codes.cpu().numpy(), c) and np.array_equal(scales.cpu().numpy(), s)
+    assert np.array_equal(to_np(back), O.mx4_dequantize(c, s), equal_nan=True)
+    device_clean()
