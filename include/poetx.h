@@ -362,13 +362,17 @@ poetx_status poetx_adamw_reset(long long n, float* m, float* v, poetx_stream str
  * and per element, in float32 with one rounding per operation for the moments:
  *   m <- beta1 m + (1 - beta1) g;   v <- beta2 v + ((1 - beta2) g) g;   r = sqrt(v);
  *   p <- p - eta * (decay * p + (m / (1 - beta1^t)) / (r / sqrt(1 - beta2^t) + eps)).
+ * Only the moments are rounded operation by operation.  The update of p multiplies by an approximate reciprocal of
+ * the denominator (off by one unit in the last place) and fuses products with sums: p is within
+ * 2^-20 * eta * (decay |p| + (beta1 |m| + (1 - beta1) |g|) / (1 - beta1^t) / (r / sqrt(1 - beta2^t) + eps)) + 2^-23 |p|
+ * of the exact result, before a bf16 p is rounded.  An eps under 2^-126 counts as 2^-126.
  * POETX_MOMENT_F32: m and v float32 [n]; scale unused.
  * POETX_MOMENT_E4M3: POETX_MOMENT_BLOCK = 256 consecutive elements of the tensor (the last block may be
  *   shorter) share scale[block] = {u_m, u_r} with u_m = max |m| / 448 and u_r = max r / 448; m and v hold one
  *   e4m3 code per element (uint8 [n]; float8_e4m3fn of other libraries) with m = u_m * code(m) and
  *   sqrt(v) = u_r * code(v).  Before rounding to a code, m and r are multiplied by 448 * (1 / max), and
- *   u = max * (1 / 448), each operation rounded to float32.  All-zero codes and scales are the moments' start.  The step uses the moments
- *   before they are rounded; r > 0 is never stored as 0 (at least 2^-9 u_r), so an element whose
+ *   u = max * (1 / 448), each operation rounded to float32.  All-zero codes and scales are the moments' start.  The
+ *   step uses the moments before they are rounded; r > 0 is never stored as 0 (at least 2^-9 u_r), so an element whose
  *   gradients were seen is never divided by eps alone.  A block whose largest |m| is under 2^-100 stores
  *   zeros; a NaN or infinite moment is stored as NaN and left out of its block's maximum.
  * seed == 0 rounds codes and bf16 parameters to nearest, ties to even.  seed != 0 rounds them up with the

@@ -350,3 +350,19 @@ def test_elements_past_32_bits(seed, monkeypatch):
     _check(cut, expect, seed)
     for a in (big.param[:at], m[:at], v[:at], big.scale[:at // 256]):
         assert not a.view(torch.int64).any().item()
+
+
+def test_an_eps_that_is_no_normal_number(monkeypatch):
+    # The reciprocal takes subnormal numbers for zero: such an eps counts as 2^-126, and an element that has seen no
+    # gradient (0 / eps) stays where it is.
+    xs = [_make(np.random.default_rng(5), 3000, moments, torch.float32, torch.float32) for moments in ("f32", "e4m3")]
+    for x in xs:
+        for a in (x.grad, x.m, x.v):
+            a.view(torch.uint8)[:256 * a.element_size()] = 0
+    monkeypatch.setitem(F32, "eps", 2.0 ** -126)
+    expect = [_expect(x, i, 5, 0) for i, x in enumerate(xs)]
+    MultiAdamW(xs).step(P.poetx_adamw_cfg(C["lr"], C["gamma"], C["beta1"], C["beta2"], 1e-42, C["weight_decay"]), t=5)
+    torch.cuda.synchronize()
+    for x, e in zip(xs, expect):
+        assert torch.isfinite(x.param).all().item()
+        _check(x, e, 0)
