@@ -22,7 +22,7 @@ __all__ = [
     "poetx_xq_quantize", "poetx_xq_dequantize", "poetx_xq_forward", "poetx_xq_backward", "poetx_xq_merge",
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
-    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "poetx_test_mx4_give_up", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
+    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "poetx_test_mx4_give_up", "poetx_test_gemm_give_up", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
     "poetx_mx4_quantize", "poetx_mx4_dequantize", "poetx_mx4_matmul", "poetx_mx4_forward", "poetx_mx4_backward",
     "poetx_mx4_merge", "POETX_MX4_BLOCK",
 ]
@@ -116,6 +116,7 @@ _SIGNATURES = {
     "poetx_fourperm_backward": (_I, [_D, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P]),
     "poetx_test_wait_timeout": (_I, [_LL, _P, _P]),
     "poetx_test_mx4_give_up": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _I, _LL, ctypes.POINTER(_I), _P]),
+    "poetx_test_gemm_give_up": (_I, [_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _I, _LL, _P]),
     "poetx_test_sqrt": (_I, [ctypes.c_uint, ctypes.c_uint, _P, _P]),
     "poetx_status_string": (ctypes.c_char_p, [_I]),
     "poetx_device_status": (_I, [ctypes.POINTER(ctypes.c_int)]),
@@ -589,6 +590,15 @@ def poetx_test_mx4_give_up(adjoint, n_tokens, d_in, d_out, X, codes, scales, Y, 
     _check(lib().poetx_test_mx4_give_up(1 if adjoint else 0, n_tokens, d_in, d_out, x, c, s, y, steps, limit_ns,
                                         ctypes.byref(splits), _stream(stream, dev)), "poetx_test_mx4_give_up")
     return splits.value
+
+
+def poetx_test_gemm_give_up(kind, M, N, K, a, b, b_scale, q, d, out2, steps, limit_ns, stream=None):
+    for x, name, numel in ((a, "a", M * K), (b, "b", N * K), (b_scale, "b_scale", N), (q, "q", N * 256), (d, "d", M * N),
+                           (out2, "out2", M * N)):
+        if x is not None:
+            _need(x, name, numel)
+    _check(lib().poetx_test_gemm_give_up(kind, M, N, K, _ptr(a), _ptr(b), _ptr(b_scale), _ptr(q), _ptr(d), _ptr(out2),
+                                         steps, limit_ns, _stream(stream)), "poetx_test_gemm_give_up")
 
 
 def poetx_test_sqrt(first, last, mismatches, stream=None):

@@ -196,12 +196,32 @@ __device__ __forceinline__ void epilogue1(const Epilogue& e, int z, int split, i
 }
 
 // ------------------------------------------------------------------------ tcgen05 kernel
+// Give-up probe (poetx_test_gemm_give_up; the PROBE instantiations alone): waits bounded by ns, and the grid's first
+// block gets only the first `steps` loads of its ring (the block factor's Q counts as the last one).
+struct GiveUpProbe {
+  unsigned long long ns;
+  int steps;
+};
+template <bool PROBE>
+struct BoundedWait {
+  const GiveUpProbe& probe;
+  __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity, int site) const {
+    return PROBE ? sm100::mbar_wait_limit(bar, parity, probe.ns, KID_GEMM_TC, site)
+                 : sm100::mbar_wait(bar, parity, KID_GEMM_TC, site);
+  }
+  // The producer stops before load i.
+  __device__ __forceinline__ bool stops(int i) const {
+    return PROBE && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && i >= probe.steps;
+  }
+};
+
 struct TcArgs {
   int M, N, K, splits;
   int a_zrow, a_zcol, b_zrow, b_zcol;
   int tma_store;  // plain bf16 d1 (no addend/alpha/diag/d2/splits, zrow1 = 0): TMA-store epilogue
   int b_early;    // B is not the previous launch's output: its first stages are requested before the wait
   Epilogue epi;
+  GiveUpProbe probe;
 };
 
 constexpr int TC_BM = 128;
@@ -217,8 +237,10 @@ __host__ __device__ constexpr size_t tc_smem_bytes() {
 // K=16) into a TMEM accumulator of BN fp32 columns and frees ring slots with tcgen05.commit;
 // then all four warps drain TMEM (warp w owns TMEM lanes 32w..32w+31 = tile rows) through the
 // epilogue.  Every wait is bounded (kWaitLimitNs); on a timeout the CTA records the error,
-// skips the rest of its work and still releases its TMEM.
-template <int BN, int STAGES, bool A_MN, bool B_MN>
+// skips the rest of its work and still releases its TMEM: a role that misses a tile leaves its loop, the
+// issuer then misses one too and commits no accumulator, and the last wait runs out for all (copies
+// under way have landed long before).
+template <int BN, int STAGES, bool A_MN, bool B_MN, bool PROBE = false>
 __global__ void __launch_bounds__(128)
     gemm_bf16_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmD, const TcArgs args) {
@@ -244,6 +266,7 @@ __global__ void __launch_bounds__(128)
   const int kt0 = (int)((long)KT * split / args.splits);
   const int kt1 = (int)((long)KT * (split + 1) / args.splits);
   const int nkt = kt1 - kt0;
+  const BoundedWait<PROBE> wait{args.probe};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -287,8 +310,9 @@ __global__ void __launch_bounds__(128)
     for (int i = 0; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
+      if (wait.stops(i)) break;
       if (i >= early) {
-        if (!mbar_wait(empty_bar(s), ph ^ 1u, KID_GEMM_TC, 1)) break;
+        if (!wait(empty_bar(s), ph ^ 1u, 1)) break;
         mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES);
         load_b(i, s);
       }
@@ -307,10 +331,11 @@ __global__ void __launch_bounds__(128)
   }
   if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer
-    for (int i = 0; i < nkt; ++i) {
+    int i = 0;
+    for (; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
-      if (!mbar_wait(full_bar(s), ph, KID_GEMM_TC, 2)) break;
+      if (!wait(full_bar(s), ph, 2)) break;
       tc_fence_after();
       const uint32_t sa = smem0 + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
@@ -321,12 +346,12 @@ __global__ void __launch_bounds__(128)
       }
       mma_commit(empty_bar(s));
     }
-    mma_commit(accum_bar);
+    if (i == nkt) mma_commit(accum_bar);
   }
   __syncwarp();
 
   // ---------------- epilogue: TMEM -> registers -> global
-  bool ok = mbar_wait(accum_bar, 0, KID_GEMM_TC, 3);
+  bool ok = wait(accum_bar, 0, 3);
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
   griddep_launch();
@@ -391,9 +416,10 @@ struct FuseArgs {
   long ld1;
   void* out2;     // bf16 [M, N] result of the block-diagonal factor
   long ld2;
+  GiveUpProbe probe;
 };
 
-template <bool B_MN, bool Q_MN>
+template <bool B_MN, bool Q_MN, bool PROBE = false>
 __global__ void __launch_bounds__(128, 1)
     gemm_bd_fused_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                      const __grid_constant__ CUtensorMap tmQ, const FuseArgs args) {
@@ -420,6 +446,7 @@ __global__ void __launch_bounds__(128, 1)
   const int m0 = blockIdx.y * TC_BM, n0 = blockIdx.x * BN;
   const int zq = blockIdx.x;  // the b = 256 block this tile's columns form
   const int nkt = (args.K + TC_BK - 1) / TC_BK;
+  const BoundedWait<PROBE> wait{args.probe};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
@@ -451,7 +478,7 @@ __global__ void __launch_bounds__(128, 1)
     for (int i = 0; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
-      if (!mbar_wait(empty_bar(s), ph ^ 1u, KID_GEMM_TC, 5)) { ok = false; break; }
+      if (wait.stops(i) || !wait(empty_bar(s), ph ^ 1u, 5)) { ok = false; break; }
       mbar_arrive_expect_tx(full_bar(s), STAGE_BYTES);
       const int k0 = i * TC_BK;
       const uint32_t sa = smem0 + s * STAGE_BYTES, sb = sa + A_BYTES;
@@ -466,12 +493,12 @@ __global__ void __launch_bounds__(128, 1)
     // Q's four 64-wide K chunks follow the K loop through the ring as if they were iterations
     // nkt .. nkt+3: each lands in the B half of its stage as soon as the last MMA reading that
     // stage has completed, so the load overlaps the tail of the K loop.
-    if (ok) {
+    if (ok && !wait.stops(nkt)) {
       mbar_arrive_expect_tx(q_full, STAGES * B_BYTES);
       for (int t = 0; t < STAGES; ++t) {
         const int v = nkt + t;
         const int s = v % STAGES;
-        if (!mbar_wait(empty_bar(s), ((uint32_t)(v / STAGES) & 1u) ^ 1u, KID_GEMM_TC, 6)) break;
+        if (!wait(empty_bar(s), ((uint32_t)(v / STAGES) & 1u) ^ 1u, 6)) break;
         const uint32_t sb = smem0 + s * STAGE_BYTES + A_BYTES;
         if (!Q_MN) {
           tma_load_2d(sb, &tmQ, q_full, 64 * t, zq * BN);
@@ -483,10 +510,11 @@ __global__ void __launch_bounds__(128, 1)
     }
   } else if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer: the K loop
-    for (int i = 0; i < nkt; ++i) {
+    int i = 0;
+    for (; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
-      if (!mbar_wait(full_bar(s), ph, KID_GEMM_TC, 7)) break;
+      if (!wait(full_bar(s), ph, 7)) break;
       tc_fence_after();
       const uint32_t sa = smem0 + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
@@ -497,12 +525,12 @@ __global__ void __launch_bounds__(128, 1)
       }
       mma_commit(empty_bar(s));
     }
-    mma_commit(accum_bar);
+    if (i == nkt) mma_commit(accum_bar);
   }
   __syncwarp();
 
   // ---------------- phase 1: D (TMEM) -> bf16 -> global d1 and the swizzled A tiles in the ring
-  bool ok = mbar_wait(accum_bar, 0, KID_GEMM_TC, 8);
+  bool ok = wait(accum_bar, 0, 8);
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
   griddep_launch();
@@ -541,7 +569,7 @@ __global__ void __launch_bounds__(128, 1)
 
   // ---------------- phase 2: out2 = D_tile . Q_block (second accumulator, TMEM columns 256..511)
   if (warp == 1 && lane == 0 && ok) {
-    if (mbar_wait(q_full, 0, KID_GEMM_TC, 9)) {
+    if (wait(q_full, 0, 9)) {
       tc_fence_after();
 #pragma unroll
       for (int t = 0; t < STAGES; ++t) {
@@ -553,11 +581,11 @@ __global__ void __launch_bounds__(128, 1)
           mma_bf16(tmem_d + BN, ad, bd, IDESC2, (t > 0 || kk > 0) ? 1u : 0u);
         }
       }
+      mma_commit(acc2_bar);  // without Q there is no second result: the wait for it runs out
     }
-    mma_commit(acc2_bar);
   }
   __syncwarp();
-  bool ok2 = ok && mbar_wait(acc2_bar, 0, KID_GEMM_TC, 10);
+  bool ok2 = ok && wait(acc2_bar, 0, 10);
   ok2 = __all_sync(0xffffffffu, ok2);
   tc_fence_after();
   if (ok2) {
@@ -604,6 +632,7 @@ struct WideArgs {
   long ld2;
   const float* bscale;  // Q8 only: scale of each row of the int8 B array
   int b_early;          // B's first stages are requested before griddep_wait (B is not the previous kernel's output)
+  GiveUpProbe probe;
 };
 
 constexpr int TCW_BM = 256, TCW_BN = 256, TCW_STAGES = 3;
@@ -637,7 +666,7 @@ __device__ __forceinline__ bool converters_all(bool p, int count) {
 // the converter warps.
 __host__ __device__ constexpr int tcw_threads(bool q8) { return q8 ? 128 + TCW_CONV_THREADS : 256; }
 
-template <bool B_MN, bool Q_MN, bool Q8 = false>
+template <bool B_MN, bool Q_MN, bool Q8 = false, bool PROBE = false>
 __global__ void __launch_bounds__(tcw_threads(Q8), 1)
     gemm_w256_tc(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmD,
@@ -669,6 +698,7 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
   const int zq = blockIdx.x;
   const int nkt = (args.K + TC_BK - 1) / TC_BK;
   const bool fuse = args.out2 != nullptr;
+  const BoundedWait<PROBE> wait{args.probe};
   // Ring stages used after the K loop: Q chunks 0,1 and 2,3, then the D half.
   const int sq0 = nkt % STAGES, sq1 = (nkt + 1) % STAGES, sdh = (nkt + 2) % STAGES;
 
@@ -728,21 +758,22 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
     for (int i = 0; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
+      if (wait.stops(i)) { ok = false; break; }
       if (i >= early) {
-        if (!mbar_wait(empty_bar(s), ph ^ 1u, KID_GEMM_TC, 11)) { ok = false; break; }
+        if (!wait(empty_bar(s), ph ^ 1u, 11)) { ok = false; break; }
         mbar_arrive_expect_tx(full_bar(s), stage_tx);
         load_b(i, s);
       }
       tma_load_2d(smem0 + s * STAGE_BYTES, &tmA, full_bar(s), i * TC_BK, m0);  // box 64 x 256: both halves
     }
-    if (ok && fuse) {
+    if (ok && fuse && !wait.stops(nkt)) {
       // Q's K chunks t = 0..3 into stages sq0 (t = 0, 1) and sq1 (t = 2, 3), each as soon as the
       // last MMA reading that stage has completed (virtual iterations nkt and nkt + 1).
       mbar_arrive_expect_tx(q_full, 4 * B_BYTES);
       for (int u = 0; u < 2; ++u) {
         const int v = nkt + u;
         const int s = v % STAGES;
-        if (!mbar_wait(empty_bar(s), ((uint32_t)(v / STAGES) & 1u) ^ 1u, KID_GEMM_TC, 12)) break;
+        if (!wait(empty_bar(s), ((uint32_t)(v / STAGES) & 1u) ^ 1u, 12)) break;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           const int t = 2 * u + w;
@@ -761,11 +792,12 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
   }
   if (warp == 1 && lane == 0) {
     // ---------------- MMA issuer: both halves per k step
-    for (int i = 0; i < nkt; ++i) {
+    int i = 0;
+    for (; i < nkt; ++i) {
       const int s = i % STAGES;
       const uint32_t ph = (uint32_t)(i / STAGES) & 1u;
-      if (!mbar_wait(full_bar(s), ph, KID_GEMM_TC, 13)) break;
-      if (Q8 && !mbar_wait(conv_bar(s), ph, KID_GEMM_TC, 19)) break;
+      if (!wait(full_bar(s), ph, 13)) break;
+      if (Q8 && !wait(conv_bar(s), ph, 19)) break;
       tc_fence_after();
       const uint32_t sa = smem0 + s * STAGE_BYTES, sb = sa + A_BYTES;
 #pragma unroll
@@ -778,7 +810,7 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
       }
       mma_commit(empty_bar(s));
     }
-    mma_commit(accum_bar);
+    if (i == nkt) mma_commit(accum_bar);
   } else if (Q8 && warp >= 4) {
     // ---------------- converters: codes -> bf16 scale * code in the stage's swizzled B tile.
     // Thread t converts chunks c = CT j + t (CT converter threads, j < 2048 / CT) of 8 codes each.
@@ -805,7 +837,7 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
       for (int j = 0; j < NCH; ++j) sc[j] = scn[j];
       if (B_MN && i + 1 < nkt) load_scales(i + 1, scn);  // K-major: the same rows every step
       // All converter warps agree (named barrier) before anyone reads, so a timeout ends all of them.
-      if (!converters_all(mbar_wait(full_bar(s), ph, KID_GEMM_TC, 18), CT)) break;
+      if (!converters_all(wait(full_bar(s), ph, 18), CT)) break;
       uint8_t* tile = smem + s * STAGE_BYTES + A_BYTES;
       uint2 code[NCH];
 #pragma unroll
@@ -835,7 +867,7 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
   }
   __syncwarp();
 
-  bool ok = mbar_wait(accum_bar, 0, KID_GEMM_TC, 14);
+  bool ok = wait(accum_bar, 0, 14);
   ok = __all_sync(0xffffffffu, ok);
   tc_fence_after();
   griddep_launch();
@@ -928,7 +960,7 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
     bool ok2 = ok;
     auto block_product = [&](int h) {
       if (warp == 1 && lane == 0 && ok2) {
-        if (mbar_wait(q_full, 0, KID_GEMM_TC, 15)) {
+        if (wait(q_full, 0, 15)) {
           tc_fence_after();
 #pragma unroll
           for (int t = 0; t < 4; ++t) {
@@ -941,13 +973,13 @@ __global__ void __launch_bounds__(tcw_threads(Q8), 1)
               mma_bf16(tmem_d + h * BN, ad, bd, IDESC2, (t > 0 || kk > 0) ? 1u : 0u);
             }
           }
+          mma_commit(acc2_bar);  // without Q there is no result: the wait for it runs out
         }
-        mma_commit(acc2_bar);
       }
       __syncwarp();
     };
     auto wait_product = [&](int h) {
-      if (ok2) ok2 = mbar_wait(acc2_bar, (uint32_t)h, KID_GEMM_TC, 16);
+      if (ok2) ok2 = wait(acc2_bar, (uint32_t)h, 16);
       ok2 = __all_sync(0xffffffffu, ok2);
       tc_fence_after();
     };

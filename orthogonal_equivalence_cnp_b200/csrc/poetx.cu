@@ -247,13 +247,13 @@ bool make_tmap(CUtensorMap* m, const Operand& op, uint32_t box_inner, uint32_t b
   return cudaGetDevice(&dev) == cudaSuccess && cudaSetDevice(dev) == cudaSuccess && encode();
 }
 
-template <int BN, int ST, bool AMN, bool BMN>
-poetx_status launch_tc(const GemmDesc& g, cudaStream_t st, int cls) {
+template <int BN, int ST, bool AMN, bool BMN, bool PROBE = false>
+poetx_status launch_tc(const GemmDesc& g, cudaStream_t st, int cls, GiveUpProbe probe = {}) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
   constexpr size_t smem = tc_smem_bytes<BN, ST>();
-  auto kern = gemm_bf16_tc<BN, ST, AMN, BMN>;
+  auto kern = gemm_bf16_tc<BN, ST, AMN, BMN, PROBE>;
   if (!attr_done[dev]) {
     if (!set_smem(kern, smem)) return POETX_ERR_CUDA;
     attr_done[dev] = true;
@@ -265,6 +265,7 @@ poetx_status launch_tc(const GemmDesc& g, cudaStream_t st, int cls) {
   a.M = g.M; a.N = g.N; a.K = g.K; a.splits = g.splits;
   a.a_zrow = (int)g.A.zrow; a.a_zcol = (int)g.A.zcol; a.b_zrow = (int)g.B.zrow; a.b_zcol = (int)g.B.zcol;
   a.epi = g.epi;
+  a.probe = probe;
   a.b_early = g.b_static ? 1 : 0;
   // TMA-store epilogue for a plain bf16 result batched (if at all) along columns: the map spans
   // every batch's columns, boxes of 64 columns x 32 rows.
@@ -411,14 +412,14 @@ bool bd_fusable(int dt, int b, const GemmDesc& g) {
          g.b_mx4 == nullptr;
 }
 
-template <bool BMN, bool QMN>
+template <bool BMN, bool QMN, bool PROBE = false>
 poetx_status launch_bd_fused(const GemmDesc& g, const void* Q, long q_rows, void* out2, long ld2, cudaStream_t st,
-                             int cls) {
+                             int cls, GiveUpProbe probe = {}) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
   constexpr size_t smem = tc_smem_bytes<256, 4>();
-  auto kern = gemm_bd_fused_tc<BMN, QMN>;
+  auto kern = gemm_bd_fused_tc<BMN, QMN, PROBE>;
   if (!attr_done[dev]) {
     if (!set_smem(kern, smem)) return POETX_ERR_CUDA;
     attr_done[dev] = true;
@@ -431,6 +432,7 @@ poetx_status launch_bd_fused(const GemmDesc& g, const void* Q, long q_rows, void
   a.M = g.M; a.N = g.N; a.K = g.K;
   a.d1 = g.epi.d1; a.ld1 = g.epi.ld1;
   a.out2 = out2; a.ld2 = ld2;
+  a.probe = probe;
   dim3 grid(g.N / 256, (g.M + TC_BM - 1) / TC_BM, 1);
   LaunchScope ls(cls, st);
   if (launch_pdl(kern, grid, dim3(128), smem, st, ta, tb, tq, a) != cudaSuccess) return POETX_ERR_CUDA;
@@ -459,14 +461,14 @@ bool w256_ok(int dt, const GemmDesc& g) {
          4L * ((g.M + TCW_BM - 1) / TCW_BM) * (g.N / TCW_BN) >= 3L * kNumSms;
 }
 
-template <bool BMN, bool QMN, bool Q8 = false>
+template <bool BMN, bool QMN, bool Q8 = false, bool PROBE = false>
 poetx_status launch_w256(const GemmDesc& g, const void* Q, long q_rows, void* out2, long ld2, cudaStream_t st,
-                         int cls) {
+                         int cls, GiveUpProbe probe = {}) {
   static bool attr_done[kMaxDevices] = {};
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= kMaxDevices) return POETX_ERR_CUDA;
   constexpr size_t smem = tcw_smem_bytes();
-  auto kern = gemm_w256_tc<BMN, QMN, Q8>;
+  auto kern = gemm_w256_tc<BMN, QMN, Q8, PROBE>;
   if (!attr_done[dev]) {
     if (!set_smem(kern, smem)) return POETX_ERR_CUDA;
     attr_done[dev] = true;
@@ -495,6 +497,7 @@ poetx_status launch_w256(const GemmDesc& g, const void* Q, long q_rows, void* ou
   a.out2 = out2; a.ld2 = ld2;
   a.bscale = g.b_scale;
   a.b_early = g.b_static ? 1 : 0;
+  a.probe = probe;
   dim3 grid(g.N / TCW_BN, (g.M + TCW_BM - 1) / TCW_BM, 1);
   LaunchScope ls(cls, st);
   if (launch_pdl_prio(kern, grid, dim3(tcw_threads(Q8)), smem, st, true, ta, tb, tq, td, to, a) != cudaSuccess)
@@ -2305,6 +2308,33 @@ poetx_status poetx_test_sqrt(unsigned first, unsigned last, unsigned long long* 
   LaunchScope ls(POETX_KC_ELEMENTWISE, stream);
   sqrt_probe_kernel<<<kNumSms * 8, 256, 0, stream>>>(first, last, mismatches);
   return last_launch();
+}
+
+poetx_status poetx_test_gemm_give_up(int kind, int M, int N, int K, const void* a, const void* b, const float* b_scale,
+                                     const void* q, void* d, void* out2, int steps, long long limit_ns,
+                                     poetx_stream stream) {
+  if (kind < 0 || kind > 3 || M <= 0 || N <= 0 || K <= 0 || N % 256 || K % 64 || limit_ns < 1000 ||
+      limit_ns > 100000000 || steps < 0)
+    return POETX_ERR_INVALID_ARG;
+  const bool q8 = kind == 3, factor = kind == 1 || (kind > 1 && out2 != nullptr);
+  POETX_TRY(check_ptrs({a, b, d}));
+  if (q8) POETX_TRY(check_ptrs({b_scale}));
+  if (factor) POETX_TRY(check_ptrs({q, out2}));
+  // The block must miss something: a step of K, or its Q.
+  if (steps > K / 64 || (steps == K / 64 && !factor)) return POETX_ERR_INVALID_ARG;
+  GemmDesc g;
+  g.M = M; g.N = N; g.K = K;
+  g.A = view(a, M, K, K);
+  g.B = view(b, N, K, K);
+  g.b_scale = q8 ? b_scale : nullptr;
+  g.epi.d1 = d; g.epi.d1_dtype = BF16; g.epi.ld1 = N;
+  POETX_TRY(check_gemm(g, BF16));
+  const GiveUpProbe probe = {(unsigned long long)limit_ns, steps};
+  const int cls = POETX_KC_TEST_GEMM;
+  if (kind == 0) return launch_tc<64, 4, false, false, true>(g, stream, cls, probe);
+  if (kind == 1) return launch_bd_fused<false, false, true>(g, q, N, out2, N, stream, cls, probe);
+  if (kind == 2) return launch_w256<false, false, false, true>(g, q, N, out2, N, stream, cls, probe);
+  return launch_w256<false, false, true, true>(g, q, N, out2, N, stream, cls, probe);
 }
 
 poetx_status poetx_test_gemm(int dtype, int M, int N, int K, int batch, int splits, const void* a, long long a_rows,

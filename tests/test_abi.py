@@ -213,3 +213,16 @@ def test_binding_checks_sizes_types_and_devices_before_calling():
         P.poetx_forward(d, 64, _FakeCuda(64 * 512 - 8, torch.bfloat16), None, None, None, None, None, None, None, None)
     with pytest.raises(ValueError, match="exceeds"):
         P.poetx_check_permutation(np.arange(4, dtype=np.int32), 5)
+
+
+@pytest.mark.parametrize("args,code", [
+    ((4, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((0, 0, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1),
+    ((0, 8, 128, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((0, 8, 256, 96, 1, 1, None, None, 1, None, 0, 1000), 1),
+    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 1, 1000), 1), ((1, 8, 256, 64, 1, 1, None, 1, 1, 1, 2, 1000), 1),
+    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 0, 999), 1), ((1, 8, 256, 64, 1, 1, None, None, 1, 1, 0, 1000), 1),
+    ((3, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((2, 8, 256, 64, None, 1, None, None, 1, None, 0, 1000), 1),
+])
+def test_give_up_probe_of_the_products_refuses_bad_calls(args, code):
+    A = 1 << 20
+    args = args[:4] + tuple(A if x == 1 else x for x in args[4:10]) + args[10:]
+    assert P.lib().poetx_test_gemm_give_up(*args, None) == code
