@@ -203,24 +203,24 @@ def oracle_step(inp: I.LayerInputs, W0p, n_tok: int):
 
 
 def measure_xq(s, src, X, dY, flush, stream, world, dev, use_graph, Kx):
-    """POET-XQ beside POET-Xmem on the same layer state: one mem-mode layer with the bf16 W0' and
-    one with W0' quantised to int8 codes and per-row scales (the W0' GEMMs dequantise in shared
-    memory).  Each step is captured and timed like the headline step (L2 flushed between steps,
-    outside the intervals), then replayed once more with the library's per-launch events to get
-    the W0' GEMM launch times."""
+    """The quantised weights beside POET-Xmem on the same layer state: one mem-mode layer with the bf16 W0',
+    one with int8 codes and per-row scales (POET-XQ; the W0' GEMMs dequantise in shared memory) and one with 4-bit
+    codes and a scale per 32 columns (MX4; the block factors are launches of their own).  Each step is
+    captured and timed like the headline step (L2 flushed between steps, outside the intervals), then
+    replayed once more with the library's per-launch events to get the W0' GEMM launch times."""
     import torch
 
     import orthogonal_equivalence_cnp_b200 as P
     from orthogonal_equivalence_cnp_b200.layer import PoetxLayer, make_desc
     res = {}
-    for name in ("mem_bf16", "xq"):
+    for name in ("mem_bf16", "xq", "mx4"):
         L = PoetxLayer(make_desc(s.d_in, s.d_out, s.b, s.k, "bf16", "mem"), s.n_tokens, device=dev)
         L.W0p.copy_(src.W0p)
         L.theta.copy_(src.theta)
         L.perm_L.copy_(src.perm_L)
         L.perm_R.copy_(src.perm_R)
-        if name == "xq":
-            L.quantize()
+        if name != "mem_bf16":
+            L.quantize("int8" if name == "xq" else "mx4")
         for _ in range(3):
             L.step(X, dY)
         torch.cuda.synchronize()
@@ -257,14 +257,16 @@ def measure_xq(s, src, X, dY, flush, stream, world, dev, use_graph, Kx):
             res[f"{name}_{tag}"] = round(ms / max(n, 1), 4)
         st, det = P.poetx_device_status()
         if st != 0:
-            raise RuntimeError(f"device-side timeout in the POET-XQ measurement ({det:#x})")
+            raise RuntimeError(f"device-side timeout in the quantised layers' measurement ({det:#x})")
         del g, L
     res["w0p_bytes_bf16"] = 2 * s.d_out * s.d_in
     res["w0p_bytes_xq"] = s.d_out * s.d_in + 4 * s.d_out
-    res["xq_over_mem_bf16_time"] = round(res["xq_ms_per_step"] / res["mem_bf16_ms_per_step"], 3)
+    res["w0p_bytes_mx4"] = s.d_out * s.d_in * 17 // 32
+    for name in ("xq", "mx4"):
+        res[f"{name}_over_mem_bf16_time"] = round(res[f"{name}_ms_per_step"] / res["mem_bf16_ms_per_step"], 3)
     res["what"] = ("POET-Xmem step (CNP, forward, backward with recompute) with W0' in bf16 vs. int8 codes + "
-                   "per-row fp32 scales dequantised inside the W0' GEMMs (three W0' launches per step: forward, "
-                   "recompute, adjoint)")
+                   "per-row fp32 scales (xq) and 4-bit codes + E8M0 scales of 32 columns (mx4), both dequantised inside "
+                   "the W0' GEMMs (three W0' launches per step: forward, recompute, adjoint)")
     return res
 
 
@@ -919,7 +921,7 @@ def main():
     ap.add_argument("--workload", choices=sorted(I.WORKLOADS) + sorted(I.STACKS), default=DEFAULT_WORKLOAD)
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-xq", dest="xq", action="store_false",
-                    help="skip timing the POET-XQ (int8 W0') mem-mode step beside the bf16 mem-mode step")
+                    help="skip timing the mem-mode step on an int8 (POET-XQ) and a 4-bit (MX4) W0' beside the bf16 one")
     ap.add_argument("--no-comparator", dest="comparator", action="store_false",
                     help="skip timing the weight-centric comparator")
     ap.add_argument("--no-graph", action="store_true", help="launch every step directly instead of replaying a CUDA graph")
