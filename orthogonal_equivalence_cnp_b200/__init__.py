@@ -324,6 +324,8 @@ def poetx_adamw_multi_step(cfg, n_tensors, tensors, t, seed=0, stream=None):
     torch tensors and checks them)."""
     if n_tensors > len(tensors):
         raise ValueError(f"n_tensors = {n_tensors} exceeds the array's {len(tensors)} entries")
+    if seed >> 64 > 0:
+        raise ValueError("seed: 64 bits")  # cut to them, a multiple of 2^64 would round to nearest
     _check(lib().poetx_adamw_multi_step(cfg, n_tensors, tensors, t, seed, _stream(stream)), "poetx_adamw_multi_step")
 
 

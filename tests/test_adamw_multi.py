@@ -115,3 +115,12 @@ def test_sqrt_probe_refusals():
     assert L.poetx_test_sqrt(0x0D7FFFFF, 0x3F800000, A, None) == 1 and L.poetx_test_sqrt(0x3F800000, 0x7F800000, A, None) == 1
     assert L.poetx_test_sqrt(2, 1, A, None) == 1 and L.poetx_test_sqrt(0x3F800000, 0x3F800000, None, None) == 1
     assert L.poetx_test_sqrt(0x3F800000, 0x3F800000, A + 4, None) == 3
+
+
+def test_seeds_of_more_than_64_bits_are_refused():
+    # Cut to 64 bits, 2^64 would be 0: to nearest, without a word.
+    for seed in (1 << 64, (1 << 64) + 1, 1 << 80):
+        with pytest.raises(ValueError, match="64 bits"):
+            P.poetx_adamw_multi_step(GOOD, 0, (P.poetx_adamw_tensor * 1)(), 1, seed, 0)
+    for seed in (0, 1, (1 << 64) - 1, -1):
+        P.poetx_adamw_multi_step(GOOD, 0, (P.poetx_adamw_tensor * 1)(), 1, seed, 0)
