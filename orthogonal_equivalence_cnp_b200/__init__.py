@@ -22,7 +22,8 @@ __all__ = [
     "poetx_xq_quantize", "poetx_xq_dequantize", "poetx_xq_forward", "poetx_xq_backward", "poetx_xq_merge",
     "poetx_check_permutation", "poetx_test_wait_timeout", "poetx_cnp_forward", "poetx_fourperm_workspace_size",
     "poetx_fourperm_forward", "poetx_fourperm_backward",
-    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "poetx_test_mx4_give_up", "poetx_test_gemm_give_up", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
+    "poetx_adamw_tensor", "poetx_adamw_multi_step", "poetx_test_sqrt", "poetx_test_mx4_give_up",
+    "poetx_test_gemm_give_up", "POETX_MOMENT_F32", "POETX_MOMENT_E4M3", "POETX_MOMENT_BLOCK",
     "poetx_mx4_quantize", "poetx_mx4_dequantize", "poetx_mx4_matmul", "poetx_mx4_forward", "poetx_mx4_backward",
     "poetx_mx4_merge", "POETX_MX4_BLOCK",
 ]

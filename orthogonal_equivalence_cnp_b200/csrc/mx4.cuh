@@ -177,8 +177,8 @@ constexpr int MX4_FEW_RT = 2;                   // forward: 16-row tiles per blo
 constexpr int MX4_FEW_ROWS = 16 * MX4_FEW_RT;   // features of a forward block
 constexpr int MX4_FEW_COLS = 128;               // features of an adjoint block
 // Warps of a block.  One token, 4096 x 14336 (31.2 MB of codes and scales, 4.8 us at the copy rate): forward 12.7 us
-// with 4 warps and 4 blocks per SM, 13.5 with 8 and 2, 14.9 with 16 rows a block (12.2, 2.6 TB/s, since the sums
-// meet no bank twice); adjoint 17.5 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
+// with 4 warps and 4 blocks per SM, 13.5 with 8 and 2, 14.9 with 16 rows a block (12.3, 2.5 TB/s, since the sums
+// meet no bank twice); adjoint 17.5 to 18.5 with 8 warps, 29 with 4 (too few warps for its 32 column tiles).
 __host__ __device__ constexpr int mx4_few_warps(bool adj) { return adj ? 8 : 4; }
 // A warp's sums in shared memory: [token][feature], a feature's place and the tokens' stride such that both the
 // accumulators' stores (eight features 1 or 16 apart, four pairs of tokens) and the reads along the features meet
@@ -522,8 +522,8 @@ __global__ void __launch_bounds__(mx4_few_warps(true) * 32, 2) mx4_few_adjoint(c
 // MN-major) in the slot that X's tile of the step lands in; one thread issues tcgen05.mma; the accumulators have
 // features in TMEM lanes, tokens in columns.  Where the tiles alone do not fill the SMs, a cluster of 2 or 4 CTAs splits
 // K and each CTA sums its share of the tokens over the cluster's shared memory, in a fixed order.
-// 2048 tokens, 4096 x 4096: 50.2 us (1.37 PFLOP/s; the tensor core is busy three quarters of the time) in short
-// runs, 59.9 in long ones under the power cap, where the library's product with a bf16 weight takes 56.1.
+// 2048 tokens, 4096 x 4096: 49.9 us (1.38 PFLOP/s; the tensor core is busy three quarters of the time) in short
+// runs, 57.8 in long ones under the power cap, where the library's product with a bf16 weight takes 47.2 and 54.2.
 struct Mx4Args {
   int M, N, K;           // features out, tokens, features in
   int TN, mt;            // tokens per tile; tiles along the features
@@ -699,8 +699,9 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
     const uint32_t cpiece = (uint32_t)((ADJ ? 0 : 2 * KA * group) + 2 * piece);
     const uint32_t c0 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + ((cpiece ^ ckey) << 4);
     const uint32_t c1 = (uint32_t)((row + (ADJ ? group * BK : 0)) * CROW) + (((cpiece + 1) ^ ckey) << 4);
-    // The two scales of a step, loaded two steps ahead (eight cost a longer loop body: 2 % more time).  Rows and features past the end repeat the last
-    // (what they give is never stored); past the end of K, where codes and tokens are zeros, any finite scale does.
+    // The two scales of a step, loaded two steps ahead (eight cost a longer loop body: 2 % more time).  Rows and
+    // features past the end repeat the last (what they give is never stored); past the end of K, where codes and
+    // tokens are zeros, any finite scale does.
     const int nblock = (int)a.pitch;
     const bool even = a.pitch % 2 == 0;
     const uint8_t* scale_at;
@@ -774,8 +775,9 @@ __global__ void __launch_bounds__(MX4_THREADS, 1)
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(ready(t));
-        // Only now have the codes been used: given back right after their loads, before the wait above, a refill
-        // was seen to overtake the loads.
+        // Every lane has used its codes, fenced its reads of them against the asynchronous copy that refills the
+        // tile, and met the others: only then is it given back.  Given back right after the loads, without the fence,
+        // refills were seen to overtake them (which of the two was missing was not taken apart: both hold here).
         mbar_arrive(cempty(s));
       }
       if (++s == a.cs) { s = 0; s_phase ^= 1u; }
