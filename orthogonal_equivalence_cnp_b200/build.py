@@ -30,7 +30,7 @@ def needs_build() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = sources() + [os.path.join(ROOT, "include", "poetx.h"), os.path.abspath(__file__)]
+    deps = sources() + [os.path.join(ROOT, "include", h) for h in ("poetx.h", "poetx_testing.h")] + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
 

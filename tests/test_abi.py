@@ -226,3 +226,12 @@ def test_give_up_probe_of_the_products_refuses_bad_calls(args, code):
     A = 1 << 20
     args = args[:4] + tuple(A if x == 1 else x for x in args[4:10]) + args[10:]
     assert P.lib().poetx_test_gemm_give_up(*args, None) == code
+
+
+def test_a_changed_header_or_source_asks_for_a_new_build(monkeypatch):
+    from orthogonal_equivalence_cnp_b200 import build
+    real = os.path.getmtime
+    newest = real(build.LIB) + 10
+    for changed in ("poetx.h", "poetx_testing.h", "poetx.cu", "mx4.cuh"):
+        monkeypatch.setattr(os.path, "getmtime", lambda p: newest if os.path.basename(p) == changed else min(real(p), newest - 10))
+        assert build.needs_build(), changed
