@@ -45,7 +45,7 @@ poetx_status poetx_test_gemm(int dtype, int M, int N, int K, int batch, int spli
 poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_stream stream);
 
 /* Failure-detection probe of the tcgen05 products D = A . B^T (A [M, K], B [N, K], D [M, N], row-major bf16; N a multiple
- * of 256, K of 64): the kernel of `kind` with its waits bounded by limit_ns (1 us .. 100 ms), whose first block loads only
+ * of 256, K of 64): the kernel of `kind` with its waits bounded by limit_ns (1 ms .. 100 ms), whose first block loads only
  * its first `steps` tiles of K.
  *   kind 0: the generic kernel, 128 x 64 tiles         kind 1: with the block factor, 128 x 256 tiles
  *   kind 2: 256 x 256 tiles, with the block factor if out2 is not NULL       kind 3: as 2, B int8 codes with b_scale [N]
@@ -58,7 +58,7 @@ poetx_status poetx_test_gemm_give_up(int kind, int M, int N, int K, const void* 
                                      poetx_stream stream);
 
 /* Failure-detection probe of the many-token MX4 product: poetx_mx4_matmul's tensor-core kernel with its waits bounded
- * by limit_ns (1 us .. 100 ms), whose first block copies only the first `steps` steps of its codes (rounded up to
+ * by limit_ns (1 ms .. 100 ms), whose first block copies only the first `steps` steps of its codes (rounded up to
  * pairs).  That block's waits run out: it records a device timeout (detail (9 << 8) | site) and returns
  * with its tile of Y as it was, and so do the blocks of its cluster; every other tile is computed as ever.  *splits (a HOST int)
  * receives the number of blocks of a cluster.  Errors as poetx_mx4_matmul, and INVALID_ARG (n_tokens <= 0, the limit out of

@@ -2263,11 +2263,15 @@ poetx_status poetx_test_wait_timeout(long long limit_ns, int* returned, poetx_st
   return last_launch();
 }
 
+// Shortest limit of the give-up probes: a block that gives up leaves when its last wait has run out, so one wait has to
+// be longer than copies are under way (microseconds).
+constexpr long long kProbeLeastNs = 1000000;
+
 poetx_status poetx_test_mx4_give_up(int adjoint, int n_tokens, int d_in, int d_out, const void* X, const uint8_t* codes,
                                     const uint8_t* scales, void* Y, int steps, long long limit_ns, int* splits,
                                     poetx_stream stream) {
-  if ((adjoint != 0 && adjoint != 1) || n_tokens <= 0 || steps < 0 || limit_ns < 1000 || limit_ns > 100000000 ||
-      splits == nullptr)
+  if ((adjoint != 0 && adjoint != 1) || n_tokens <= 0 || steps < 0 || limit_ns < kProbeLeastNs ||
+      limit_ns > 100000000 || splits == nullptr)
     return POETX_ERR_INVALID_ARG;
   POETX_TRY(check_mx4(d_in, d_out, n_tokens));
   POETX_TRY(check_ptrs({X, codes, scales, Y}));
@@ -2313,7 +2317,7 @@ poetx_status poetx_test_sqrt(unsigned first, unsigned last, unsigned long long* 
 poetx_status poetx_test_gemm_give_up(int kind, int M, int N, int K, const void* a, const void* b, const float* b_scale,
                                      const void* q, void* d, void* out2, int steps, long long limit_ns,
                                      poetx_stream stream) {
-  if (kind < 0 || kind > 3 || M <= 0 || N <= 0 || K <= 0 || N % 256 || K % 64 || limit_ns < 1000 ||
+  if (kind < 0 || kind > 3 || M <= 0 || N <= 0 || K <= 0 || N % 256 || K % 64 || limit_ns < kProbeLeastNs ||
       limit_ns > 100000000 || steps < 0)
     return POETX_ERR_INVALID_ARG;
   const bool q8 = kind == 3, factor = kind == 1 || (kind > 1 && out2 != nullptr);

@@ -216,11 +216,11 @@ def test_binding_checks_sizes_types_and_devices_before_calling():
 
 
 @pytest.mark.parametrize("args,code", [
-    ((4, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((0, 0, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1),
-    ((0, 8, 128, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((0, 8, 256, 96, 1, 1, None, None, 1, None, 0, 1000), 1),
-    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 1, 1000), 1), ((1, 8, 256, 64, 1, 1, None, 1, 1, 1, 2, 1000), 1),
-    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 0, 999), 1), ((1, 8, 256, 64, 1, 1, None, None, 1, 1, 0, 1000), 1),
-    ((3, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1000), 1), ((2, 8, 256, 64, None, 1, None, None, 1, None, 0, 1000), 1),
+    ((4, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1_000_000), 1), ((0, 0, 256, 64, 1, 1, None, None, 1, None, 0, 1_000_000), 1),
+    ((0, 8, 128, 64, 1, 1, None, None, 1, None, 0, 1_000_000), 1), ((0, 8, 256, 96, 1, 1, None, None, 1, None, 0, 1_000_000), 1),
+    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 1, 1_000_000), 1), ((1, 8, 256, 64, 1, 1, None, 1, 1, 1, 2, 1_000_000), 1),
+    ((0, 8, 256, 64, 1, 1, None, None, 1, None, 0, 999_999), 1), ((1, 8, 256, 64, 1, 1, None, None, 1, 1, 0, 1_000_000), 1),
+    ((3, 8, 256, 64, 1, 1, None, None, 1, None, 0, 1_000_000), 1), ((2, 8, 256, 64, None, 1, None, None, 1, None, 0, 1_000_000), 1),
 ])
 def test_give_up_probe_of_the_products_refuses_bad_calls(args, code):
     A = 1 << 20

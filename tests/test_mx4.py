@@ -92,15 +92,15 @@ def test_binding_checks_types_and_sizes():
 
 
 @pytest.mark.parametrize("args,code", [
-    ((0, 64, 512, 512, A, A, A, 2 * A, 0, 999), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 0, 100_000_001), 1),
-    ((0, 64, 512, 512, A, A, A, 2 * A, -1, 1000), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 1 << 30, 1000), 1),
-    ((0, 0, 512, 512, A, A, A, 2 * A, 0, 1000), 1), ((0, 64, 500, 512, A, A, A, 2 * A, 0, 1000), 2),
-    ((0, 64, 512, 512, A, A, A, A, 0, 1000), 1), ((0, 64, 512, 512, A, A + 8, A, 2 * A, 0, 1000), 3),
+    ((0, 64, 512, 512, A, A, A, 2 * A, 0, 999_999), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 0, 100_000_001), 1),
+    ((0, 64, 512, 512, A, A, A, 2 * A, -1, 1_000_000), 1), ((0, 64, 512, 512, A, A, A, 2 * A, 1 << 30, 1_000_000), 1),
+    ((0, 0, 512, 512, A, A, A, 2 * A, 0, 1_000_000), 1), ((0, 64, 500, 512, A, A, A, 2 * A, 0, 1_000_000), 2),
+    ((0, 64, 512, 512, A, A, A, A, 0, 1_000_000), 1), ((0, 64, 512, 512, A, A + 8, A, 2 * A, 0, 1_000_000), 3),
 ])
 def test_give_up_probe_refusals(args, code):
     splits = ctypes.c_int()
     assert P.lib().poetx_test_mx4_give_up(*args, ctypes.byref(splits), None) == code
-    assert P.lib().poetx_test_mx4_give_up(0, 64, 512, 512, A, A, A, 2 * A, 0, 1000, None, None) == 1
+    assert P.lib().poetx_test_mx4_give_up(0, 64, 512, 512, A, A, A, 2 * A, 0, 1_000_000, None, None) == 1
 
 
 @pytest.mark.parametrize("adjoint", [0, 1])
