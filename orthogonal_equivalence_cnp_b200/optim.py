@@ -44,7 +44,8 @@ class MultiAdamW:
     """The tensors of one optimiser on one device.  Keeps references to them; their addresses must
     not change while it is used (gradients are written in place, as the layers and GradBuckets do).
     All of them share one step count: tensors whose moments restart at different times (theta, which a
-    merge restarts, and norms or embeddings, which it does not) take an object each."""
+    merge restarts, and norms or embeddings, which it does not) take an object each.  Its state, as a checkpoint
+    keeps it, is every tensor's m, v and scale and the step count t."""
 
     def __init__(self, tensors):
         self.tensors = [x if isinstance(x, AdamWTensor) else AdamWTensor(*x) for x in tensors]

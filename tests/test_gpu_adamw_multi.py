@@ -366,3 +366,21 @@ def test_an_eps_that_is_no_normal_number(monkeypatch):
     for x, e in zip(xs, expect):
         assert torch.isfinite(x.param).all().item()
         _check(x, e, 0)
+
+
+def test_state_saved_and_loaded_goes_on_with_the_same_bits():
+    rng = np.random.default_rng(6)
+    xs = [_make(rng, n, "e4m3" if n % 2 else "f32", torch.bfloat16, torch.float32) for n in (5001, 300, 77)]
+    opt = MultiAdamW(xs)
+    for seed in (1, 2):
+        opt.step(_cfg(), seed=seed)
+    saved = [[None if a is None else a.cpu() for a in x[:5]] for x in opt.tensors]
+    ys = [AdamWTensor(*(None if a is None else a.cuda() for a in s)) for s in saved]
+    again = MultiAdamW(ys)
+    again.t = opt.t
+    for o in (opt, again):
+        o.step(_cfg(), seed=3)
+    for x, y in zip(xs, ys):
+        assert all(a is None or torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(x[:5], y[:5]))
+    opt.reset(stream=0)  # the default stream by its handle
+    assert opt.t == 0 and not any(x.m.view(torch.uint8).any().item() for x in xs)
